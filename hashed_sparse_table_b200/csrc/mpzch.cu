@@ -3,6 +3,7 @@
 #include "mpzch.h"
 #include "mpzch_internal.h"
 #include "mpzch_kernels.cuh"
+#include "mpzch_launch.cuh"
 #include "mpzch_tier.cuh"
 
 #include <cuda_runtime.h>
@@ -16,6 +17,7 @@
 #include <vector>
 
 using namespace mpzch;
+using namespace mpzch_internal;
 
 namespace {
 
@@ -60,135 +62,6 @@ int host_mapped_alloc(void** dev_ptr, void** host_ptr, size_t bytes) {
     cudaFreeHost(*host_ptr);
     *host_ptr = nullptr;
     *dev_ptr = nullptr;
-    return MPZCH_ECUDA;
-  }
-  return MPZCH_OK;
-}
-
-inline cudaStream_t S(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-
-int sm_count() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 148;
-  }
-  return n;
-}
-
-// Grid for a grid-stride kernel: enough blocks for `work` threads, at most
-// `per_sm` resident blocks on every SM.
-unsigned grid_for(int64_t work_threads, int block, int per_sm = 8) {
-  int64_t g = (work_threads + block - 1) / block;
-  const int64_t cap = (int64_t)sm_count() * per_sm;
-  if (g > cap) g = cap;
-  if (g < 1) g = 1;
-  return (unsigned)g;
-}
-
-// Blocks of `kern` (with `block` threads, `smem` dynamic bytes) resident on
-// one SM, looked up once per kernel and device; at least 1.
-int resident_blocks(const void* kern, int block, size_t smem) {
-  struct Entry {
-    const void* kern;
-    int device, block;
-    size_t smem;
-    int blocks;
-  };
-  static std::mutex mu;
-  static std::vector<Entry> done;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  for (const Entry& e : done)
-    if (e.kern == kern && e.device == dev && e.block == block && e.smem == smem) return e.blocks;
-  int b = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kern, block, smem) != cudaSuccess) {
-    cudaGetLastError();
-    b = 1;
-  }
-  if (b < 1) b = 1;
-  done.push_back({kern, dev, block, smem, b});
-  return b;
-}
-
-int after_launch() {
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError() == cudaSuccess ? MPZCH_OK : MPZCH_ECUDA;
-}
-
-// Raises a kernel's dynamic shared-memory limit to `bytes` on the current
-// device, once per (kernel, device) and size: the attribute belongs to the
-// kernel function on one device, so kernels sharing a signature (template
-// instances) and devices are tracked separately.
-int allow_dynamic_smem(const void* kern, size_t bytes) {
-  struct Entry {
-    const void* kern;
-    int device;
-    size_t bytes;
-  };
-  static std::mutex mu;
-  static std::vector<Entry> done;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MPZCH_ECUDA;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const Entry& e : done)
-    if (e.kern == kern && e.device == dev && e.bytes >= bytes) return MPZCH_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return MPZCH_ECUDA;
-  }
-  done.push_back({kern, dev, bytes});
-  return MPZCH_OK;
-}
-
-// Launches a kernel; with `pdl` it may start while the previous kernel of the
-// stream drains (programmatic dependent launch: every kernel waits for its
-// predecessors with griddepcontrol.wait before touching memory).
-template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, bool pdl,
-           Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return MPZCH_ECUDA;
-  }
-  return MPZCH_OK;
-}
-
-template <typename... KArgs, typename... Args>
-int launch_smem(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
-                cudaStream_t st, bool pdl, Args&&... args) {
-  int rc = allow_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
-  if (rc) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
     return MPZCH_ECUDA;
   }
   return MPZCH_OK;
@@ -1533,6 +1406,7 @@ namespace mpzch_internal {
 int64_t table_capacity(const mpzch_table* t) { return t->C; }
 int32_t table_dim(const mpzch_table* t) { return t->D; }
 int table_device(const mpzch_table* t) { return t->device; }
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 int export_since(mpzch_table* t, int64_t since, int32_t* rows, int64_t* dev_count, int64_t max_rows,
                  int8_t* q, float* scale, int64_t* keys, int64_t* last, cudaStream_t st) {

@@ -1,5 +1,6 @@
-// Internal interface between the table library (mpzch.cu) and the streaming
-// exporter (mpzch_res.cu).  Not part of the public ABI.
+// Internal interface between the table library (mpzch.cu), the streaming
+// exporter (mpzch_res.cu) and the history cache (mpzch_kv.cu).  Not part of the
+// public ABI.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -11,6 +12,9 @@ namespace mpzch_internal {
 int64_t table_capacity(const mpzch_table* t);
 int32_t table_dim(const mpzch_table* t);
 int table_device(const mpzch_table* t);
+
+// One more kernel launched (mpzch_launch_count).
+void count_launch();
 
 // On stream `st` (joined with the table's other work): rows with a live key and
 // last-write step >= since, ascending, into rows[] with their number in
