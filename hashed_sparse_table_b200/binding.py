@@ -31,6 +31,10 @@ MPZCH_STATUS_BADROW = 2
 MPZCH_STATUS_BADAO = 4
 MPZCH_STATUS_INTERNAL = 8
 MPZCH_STATUS_TIMEOUT = 16
+MPZCH_STATUS_BADLEN = 32
+MPZCH_STATUS_NOBLOCK = 64
+MPZCH_STATUS_BADBLOCK = 128
+MPZCH_KV_MAX_REQUESTS = 16384
 MPZCH_NPHASES = 7
 MPZCH_OPT_WIDE_ROUNDS = 1
 MPZCH_VALUES_IN_HOST_MEMORY = 1
@@ -89,6 +93,12 @@ _SIGS = {
     "mpzch_owner_partition": [_p, _p, _i64, _p, _i32, _p, _i32, _p, _p, _p, _p, _p, _i64, _p],
     "mpzch_owner_combine": [_p, _p, _i64, _i32, _i64, _p, _p, _i32, _p, _i64, _i32, _p, _p, _p,
                             _p, _p, _p],
+    "mpzch_kv_tables": [_p, _p, _i32, _i32, _p, _i64, _p, _p, _i32, _p, _p, _p, _i64, _p, _p, _p],
+    "mpzch_kv_append": [_p, _i64, _i64, _p, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p, _i64, _i32,
+                        _i32, _i32, _p, _p],
+    "mpzch_kv_attend": [_p, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _i64, _i32, _i32, _i32, _i32,
+                        _p, _i32, _p, _p, _i32, _i32, C.c_float, _i32, _i32, _p, _i64, _i64, _p,
+                        _p, _i64, _p, _p],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -98,6 +108,8 @@ _lib.mpzch_launch_count.argtypes = []
 _lib.mpzch_launch_count.restype = _i64
 _lib.mpzch_owner_partition_workspace.argtypes = [_i64, _i32]
 _lib.mpzch_owner_partition_workspace.restype = _i64
+_lib.mpzch_kv_attend_workspace.argtypes = [_i32, _i32, _i32]
+_lib.mpzch_kv_attend_workspace.restype = _i64
 MPZCH_MAX_OWNERS = 256
 
 
@@ -462,6 +474,218 @@ def mpzch_owner_combine(send_ids, pos, n_owners: int, shard_capacity: int, recv_
         _ptr(send_ids), _ptr(pos), n, n_owners, shard_capacity, _ptr(recv_rows), _ptr(recv_feat),
         recv_feat.shape[1], _ptr(ao_table), ao_n, ao_dim, _ptr(ao_rows), _ptr(rows), _ptr(hit),
         _ptr(out), _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------------------------------ history cache
+_KV_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_workspace_bytes: dict = {}
+
+
+def _kv_bad(device: int, *named) -> ValueError:
+    """The error for the first (name, tensor, dtype) that a history call refuses."""
+    for name, t, dtype in named:
+        if t is not None and not (t.dtype is dtype and t.is_contiguous()
+                                  and t.get_device() == device):
+            return ValueError(f"{name}: expected a contiguous {dtype} tensor on cuda:{device}, the "
+                              f"current device, got {t.dtype} on {t.device} "
+                              f"(contiguous={t.is_contiguous()})")
+    return ValueError("unexpected arguments")
+
+
+def _kv_ok(t, dtype, device: int) -> bool:
+    return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+
+
+def _kv_opt(t, dtype, device: int) -> bool:
+    return t is None or _kv_ok(t, dtype, device)
+
+
+def _kv_stream(stream, device: int):
+    """The raw stream of a history call; torch's Stream object is not built for the current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
+
+
+def _kv_cache(device: int, k_cache, v_cache, k_scale, v_scale):
+    f32, i8 = torch.float32, torch.int8
+    if not (_kv_ok(k_cache, i8, device) and _kv_ok(v_cache, i8, device)
+            and _kv_ok(k_scale, f32, device) and _kv_ok(v_scale, f32, device)):
+        raise _kv_bad(device, ("k_cache", k_cache, i8), ("v_cache", v_cache, i8),
+                      ("k_scale", k_scale, f32), ("v_scale", v_scale, f32))
+    shape = k_cache.shape
+    if (len(shape) != 4 or v_cache.shape != shape or k_scale.shape != shape[:2]
+            or v_scale.shape != shape[:2]):
+        raise ValueError("expected caches [blocks, kv_heads, block_size, dim] and scales "
+                         f"[blocks, kv_heads], got {tuple(shape)}, {tuple(v_cache.shape)}, "
+                         f"{tuple(k_scale.shape)}, {tuple(v_scale.shape)}")
+    return shape
+
+
+def _kv_rows(device: int, t, name: str, n: int, heads: int, dim: int, dtype):
+    """Element strides (row, head) of [n, heads, dim] with contiguous values of a head."""
+    if t.shape == (n, heads, dim) and t.dtype is dtype and t.get_device() == device:
+        sn, sh, sd = t.stride()
+        if sd == 1:
+            return sn, sh
+    raise ValueError(f"{name}: expected [{n}, {heads}, {dim}] of {dtype} on cuda:{device}, the "
+                     f"current device, with contiguous heads, got {t.dtype} {tuple(t.shape)} with "
+                     f"strides {t.stride()} on {t.device}")
+
+
+def _kv_type(t) -> int:
+    code = _KV_TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"expected float32, float16 or bfloat16 rows, got {t.dtype}")
+    return code
+
+
+def mpzch_kv_tables(cached_len, new_len, block_size: int, free_blocks, free_count, block_table,
+                    cu_new, seq_len, slots, free_count_out, status=None, stream=None) -> None:
+    """Block tables, slots and lengths of a batch (include/mpzch.h).  block_table: int32
+    [requests, max_blocks], updated in place; cu_new: int32 [requests + 1]; slots: int64 with
+    room for every new token, -1 behind the last one."""
+    device = torch.cuda.current_device()
+    i32, i64 = torch.int32, torch.int64
+    if not (_kv_ok(cached_len, i32, device) and _kv_ok(new_len, i32, device)
+            and _kv_ok(free_blocks, i32, device) and _kv_ok(free_count, i64, device)
+            and _kv_ok(block_table, i32, device) and _kv_ok(cu_new, i32, device)
+            and _kv_ok(seq_len, i32, device) and _kv_ok(slots, i64, device)
+            and _kv_ok(free_count_out, i64, device) and _kv_opt(status, i32, device)):
+        raise _kv_bad(device, ("cached_len", cached_len, i32), ("new_len", new_len, i32),
+                      ("free_blocks", free_blocks, i32), ("free_count", free_count, i64),
+                      ("block_table", block_table, i32), ("cu_new", cu_new, i32),
+                      ("seq_len", seq_len, i32), ("slots", slots, i64),
+                      ("free_count_out", free_count_out, i64), ("status", status, i32))
+    n = cached_len.numel()
+    table = block_table.shape
+    if (new_len.numel() != n or len(table) != 2 or table[0] != n or cu_new.numel() != n + 1
+            or seq_len.numel() != n or free_count.numel() < 1 or free_count_out.numel() < 1):
+        raise ValueError(f"{n} requests need new_len [{n}], block_table [{n}, blocks], cu_new "
+                         f"[{n + 1}], seq_len [{n}] and counts of one value")
+    rc = _lib.mpzch_kv_tables(
+        cached_len.data_ptr(), new_len.data_ptr(), n, block_size, free_blocks.data_ptr(),
+        free_blocks.numel(), free_count.data_ptr(), block_table.data_ptr(), table[1],
+        cu_new.data_ptr(), seq_len.data_ptr(), slots.data_ptr(), slots.numel(),
+        free_count_out.data_ptr(), None if status is None else status.data_ptr(),
+        _kv_stream(stream, device))
+    _check("mpzch_kv_tables", rc)
+
+
+def mpzch_kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, status=None,
+                    stream=None) -> None:
+    """Appends k, v [n, kv_heads, dim] to the int8 blocks that slots (int64 [n]) name."""
+    device = torch.cuda.current_device()
+    blocks, heads, block_size, dim = _kv_cache(device, k_cache, v_cache, k_scale, v_scale)
+    if not (_kv_ok(slots, torch.int64, device) and _kv_opt(status, torch.int32, device)):
+        raise _kv_bad(device, ("slots", slots, torch.int64), ("status", status, torch.int32))
+    n = slots.numel()
+    code = _kv_type(k)
+    k_n, k_h = _kv_rows(device, k, "k", n, heads, dim, k.dtype)
+    v_n, v_h = _kv_rows(device, v, "v", n, heads, dim, k.dtype)
+    rc = _lib.mpzch_kv_append(
+        k.data_ptr(), k_n, k_h, v.data_ptr(), v_n, v_h, n, code, slots.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), blocks,
+        block_size, heads, dim, None if status is None else status.data_ptr(),
+        _kv_stream(stream, device))
+    _check("mpzch_kv_append", rc)
+
+
+def mpzch_kv_attend_workspace(q_heads: int, kv_heads: int, dim: int) -> int:
+    b = _lib.mpzch_kv_attend_workspace(q_heads, kv_heads, dim)
+    if b < 0:
+        raise MpzchError("mpzch_kv_attend_workspace", MPZCH_EINVAL)
+    return b
+
+
+def mpzch_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, seq_len,
+                    max_new: int, out, softmax_scale: Optional[float] = None, causal: bool = True,
+                    window: int = 0, lse=None, workspace=None, status=None, stream=None) -> None:
+    """Attention of q [n, q_heads, dim] over the cached histories into out (same shape and type;
+    include/mpzch.h).  softmax_scale: dim ** -0.5 unless given.  max_new: a bound on the rows of
+    one request.  workspace: uint8, mpzch_kv_attend_workspace bytes; taken from torch's allocator
+    for the current stream unless given."""
+    device = torch.cuda.current_device()
+    blocks, heads, block_size, dim = _kv_cache(device, k_cache, v_cache, k_scale, v_scale)
+    code = _kv_type(q)
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [rows, heads, dim], got {tuple(q.shape)}")
+    n, q_heads = q.shape[0], q.shape[1]
+    q_n, q_h = _kv_rows(device, q, "q", n, q_heads, dim, q.dtype)
+    o_n, o_h = _kv_rows(device, out, "out", n, q_heads, dim, q.dtype)
+    i32 = torch.int32
+    if not (_kv_ok(block_table, i32, device) and _kv_ok(cu_new, i32, device)
+            and _kv_ok(seq_len, i32, device) and _kv_opt(lse, torch.float32, device)
+            and _kv_opt(workspace, torch.uint8, device) and _kv_opt(status, i32, device)):
+        raise _kv_bad(device, ("block_table", block_table, i32), ("cu_new", cu_new, i32),
+                      ("seq_len", seq_len, i32), ("lse", lse, torch.float32),
+                      ("workspace", workspace, torch.uint8), ("status", status, i32))
+    b = seq_len.numel()
+    table = block_table.shape
+    if (len(table) != 2 or table[0] != b or cu_new.numel() != b + 1
+            or (lse is not None and lse.shape != (n, q_heads))):
+        raise ValueError(f"{b} requests of {n} rows need block_table [{b}, blocks], cu_new "
+                         f"[{b + 1}] and lse [{n}, {q_heads}]")
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("a call with a stream of its own needs a workspace too")
+        key = (device, q_heads, heads, dim)
+        size = _workspace_bytes.get(key)
+        if size is None:
+            size = _workspace_bytes[key] = mpzch_kv_attend_workspace(q_heads, heads, dim)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    rc = _lib.mpzch_kv_attend(
+        q.data_ptr(), q_n, q_h, n, code, k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), blocks, block_size, q_heads, heads, dim,
+        block_table.data_ptr(), table[1], cu_new.data_ptr(), seq_len.data_ptr(), b, max_new,
+        dim ** -0.5 if softmax_scale is None else softmax_scale, 1 if causal else 0, window,
+        out.data_ptr(), o_n, o_h, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), None if status is None else status.data_ptr(),
+        _kv_stream(stream, device))
+    _check("mpzch_kv_attend", rc)
+
+
+class MpzchHistory:
+    """An int8 history cache (codes and scales as torch tensors) with its list of free blocks and
+    the requests' block tables; methods forward to the entry points above."""
+
+    def __init__(self, num_blocks: int, block_size: int, kv_heads: int, dim: int,
+                 max_requests: int, max_blocks: int):
+        dev = torch.device("cuda", torch.cuda.current_device())
+        shape = (num_blocks, kv_heads, block_size, dim)
+        self.block_size = block_size
+        self.k_cache = torch.zeros(shape, dtype=torch.int8, device=dev)
+        self.v_cache = torch.zeros(shape, dtype=torch.int8, device=dev)
+        self.k_scale = torch.zeros(shape[:2], dtype=torch.float32, device=dev)
+        self.v_scale = torch.zeros(shape[:2], dtype=torch.float32, device=dev)
+        self.free_blocks = torch.arange(num_blocks, dtype=torch.int32, device=dev)
+        self.free_count = torch.full((1,), num_blocks, dtype=torch.int64, device=dev)
+        self.block_table = torch.full((max_requests, max_blocks), -1, dtype=torch.int32, device=dev)
+        self.seq_len = torch.zeros(max_requests, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def cache(self):
+        return self.k_cache, self.v_cache, self.k_scale, self.v_scale
+
+    def extend(self, new_len, n_slots: int, stream=None):
+        """Room for new_len[b] more tokens of every request; returns (cu_new, slots)."""
+        dev = self.seq_len.device
+        cu = torch.empty(new_len.numel() + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty(n_slots, dtype=torch.int64, device=dev)
+        seq, left = torch.empty_like(self.seq_len), torch.empty_like(self.free_count)
+        mpzch_kv_tables(self.seq_len, new_len, self.block_size, self.free_blocks, self.free_count,
+                        self.block_table, cu, seq, slots, left, self.status, stream)
+        self.seq_len, self.free_count = seq, left
+        return cu, slots
+
+    def append(self, k, v, slots, stream=None):
+        mpzch_kv_append(k, v, slots, *self.cache(), self.status, stream)
+
+    def attend(self, q, cu_new, max_new: int, out=None, stream=None, **options):
+        out = torch.empty_like(q) if out is None else out
+        mpzch_kv_attend(q, *self.cache(), self.block_table, cu_new, self.seq_len, max_new, out,
+                        status=self.status, stream=stream, **options)
+        return out
 
 
 class MpzchTable:

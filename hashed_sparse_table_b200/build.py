@@ -2,7 +2,7 @@
 
     python -m hashed_sparse_table_b200.build [--force]
 
-nvcc compiles csrc/mpzch.cu for sm_100a only, without fast-math (the Writeback
+nvcc compiles csrc/*.cu for sm_100a only, without fast-math (the Writeback
 and the int8 export rely on IEEE-rounded subtraction and division).
 """
 import os
@@ -13,10 +13,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmpzch.so")
-SOURCES = [os.path.join(CSRC, "mpzch.cu"), os.path.join(CSRC, "mpzch_res.cu")]
+SOURCES = [os.path.join(CSRC, "mpzch.cu"), os.path.join(CSRC, "mpzch_res.cu"),
+           os.path.join(CSRC, "mpzch_kv.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in
                   ("mpzch_kernels.cuh", "mpzch_tier.cuh", "mpzch_device.cuh", "mpzch_launch.cuh",
-                   "mpzch_internal.h")] + [os.path.join(ROOT, "include", "mpzch.h")]
+                   "mpzch_internal.h", "mpzch_kv_kernels.cuh", "mpzch_kv_rows.cuh")] + [os.path.join(ROOT, "include", "mpzch.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -1,0 +1,226 @@
+// libmpzch: C entry points of the history cache (include/mpzch.h, "History
+// cache").
+#include "mpzch.h"
+#include "mpzch_internal.h"
+#include "mpzch_kv_rows.cuh"
+#include "mpzch_launch.cuh"
+
+#include <cmath>
+
+using namespace mpzch_kv;
+using namespace mpzch_internal;
+
+namespace {
+
+constexpr int64_t kMaxInt = 0x7FFFFFFFll;
+
+int log2_of(int x) {
+  int k = 0;
+  while ((1 << k) < x) ++k;
+  return k;
+}
+
+bool block_size_ok(int32_t s) { return s == 16 || s == 32 || s == 64 || s == 128; }
+bool dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
+int type_bytes(int32_t t) {
+  return t == MPZCH_F32 ? 4 : t == MPZCH_F16 || t == MPZCH_BF16 ? 2 : 0;
+}
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Rows of heads: every head of every row starts on a 16-byte boundary.
+bool rows_ok(const void* p, int64_t sn, int64_t sh, int bytes) {
+  return aligned16(p) && sn >= 0 && sh >= 0 && (sn * bytes) % 16 == 0 && (sh * bytes) % 16 == 0 &&
+         sn < (1ll << 40) && sh < (1ll << 40);
+}
+
+template <typename T, int D>
+int launch_append(const AppendArgs& a, cudaStream_t st) {
+  const void* kern = reinterpret_cast<const void*>(k_kv_append<T, D>);
+  const int64_t warps = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2;
+  return launch(k_kv_append<T, D>, grid_for(warps * 32, 256, resident_blocks(kern, 256, 0)), 256,
+                st, true, a);
+}
+
+template <typename T>
+int launch_append_dim(const AppendArgs& a, int dim, cudaStream_t st) {
+  return dim == 32 ? launch_append<T, 32>(a, st)
+                   : dim == 64 ? launch_append<T, 64>(a, st) : launch_append<T, 128>(a, st);
+}
+
+int row_grid_blocks() { return sm_count() * kRowBlocksPerSm; }
+
+int64_t part_bytes(int dim) {
+  const int64_t blocks = row_grid_blocks();
+  const int64_t heads = (blocks * (int64_t)sizeof(PartHead) + 255) / 256 * 256;
+  return heads + blocks * 2 * kRowTile * (dim + 2) * (int64_t)sizeof(float);
+}
+
+template <int D, typename T, int NQ, int NP>
+int launch_rows(const AttendArgs& a, cudaStream_t st) {
+  const void* kern = reinterpret_cast<const void*>(k_kv_rows<D, T, NQ, NP>);
+  int per_sm = resident_blocks(kern, 32 * kRowWarps, 0);
+  if (per_sm > kRowBlocksPerSm) per_sm = kRowBlocksPerSm;
+  const unsigned grid = (unsigned)(sm_count() * per_sm);
+  int rc = launch(k_kv_rows<D, T, NQ, NP>, grid, 32 * kRowWarps, st, true, a);
+  if (!rc) rc = launch(k_kv_join<D, T>, grid, 256, st, true, a);
+  return rc;
+}
+
+template <typename T, int NQ, int NP>
+int launch_rows_dim(const AttendArgs& a, int dim, cudaStream_t st) {
+  return dim == 32 ? launch_rows<32, T, NQ, NP>(a, st)
+                   : dim == 64 ? launch_rows<64, T, NQ, NP>(a, st) : launch_rows<128, T, NQ, NP>(a, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mpzch_kv_tables(const int32_t* cached_len, const int32_t* new_len, int32_t n_requests,
+                    int32_t block_size, const int32_t* free_blocks, int64_t n_free_blocks,
+                    const int64_t* free_count, int32_t* block_table, int32_t max_blocks,
+                    int32_t* cu_new, int32_t* seq_len, int64_t* slots, int64_t n_slots,
+                    int64_t* free_count_out, int32_t* dev_status, void* stream) {
+  if (n_requests < 0 || n_requests > MPZCH_KV_MAX_REQUESTS || !block_size_ok(block_size) ||
+      n_free_blocks < 0 || n_free_blocks >= kMaxInt || max_blocks < 0 || n_slots < 0 ||
+      n_slots >= kMaxInt)
+    return MPZCH_EINVAL;
+  if (!free_count || !free_count_out || free_count == free_count_out || !cu_new ||
+      (n_free_blocks > 0 && !free_blocks) || (n_slots > 0 && !slots))
+    return MPZCH_EINVAL;
+  if (n_requests > 0 && (!cached_len || !new_len || !seq_len || (max_blocks > 0 && !block_table) ||
+                         seq_len == cached_len || seq_len == new_len || cu_new == cached_len ||
+                         cu_new == new_len))
+    return MPZCH_EINVAL;
+  TablesArgs a;
+  a.cached = cached_len;
+  a.news = new_len;
+  a.B = n_requests;
+  a.bs_log = log2_of(block_size);
+  a.free_blocks = free_blocks;
+  a.n_free = n_free_blocks;
+  a.free_count = reinterpret_cast<const long long*>(free_count);
+  a.table = block_table;
+  a.max_blocks = max_blocks;
+  a.cu = cu_new;
+  a.seq = seq_len;
+  a.slots = reinterpret_cast<long long*>(slots);
+  a.n_slots = n_slots;
+  a.free_out = reinterpret_cast<long long*>(free_count_out);
+  a.status = dev_status;
+  const int block = n_requests <= 1024 ? 256 : 1024;
+  const size_t smem = (size_t)n_requests * 2 * sizeof(int32_t);
+  // 8 rows or requests a thread at least, one block an SM at most
+  const int64_t work = (n_slots > n_requests ? n_slots : n_requests) / 8;
+  return launch_smem(k_kv_tables, grid_for(work, block, 1), block, smem, S(stream), true, a);
+}
+
+int mpzch_kv_append(const void* k, int64_t k_stride_n, int64_t k_stride_h, const void* v,
+                    int64_t v_stride_n, int64_t v_stride_h, int64_t n, int32_t dtype,
+                    const int64_t* slots, int8_t* k_cache, int8_t* v_cache, float* k_scale,
+                    float* v_scale, int64_t num_blocks, int32_t block_size, int32_t kv_heads,
+                    int32_t dim, int32_t* dev_status, void* stream) {
+  const int bytes = type_bytes(dtype);
+  if (n < 0 || n > kMaxInt || bytes == 0 || !block_size_ok(block_size) || !dim_ok(dim) ||
+      kv_heads < 1 || kv_heads > 4096 || num_blocks < 0 || num_blocks > kMaxInt)
+    return MPZCH_EINVAL;
+  if (n == 0) return MPZCH_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale ||
+      !rows_ok(k, k_stride_n, k_stride_h, bytes) || !rows_ok(v, v_stride_n, v_stride_h, bytes) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || k_cache == v_cache || k_scale == v_scale)
+    return MPZCH_EINVAL;
+  AppendArgs a;
+  a.x[0] = k;
+  a.x[1] = v;
+  a.sn[0] = k_stride_n;
+  a.sn[1] = v_stride_n;
+  a.sh[0] = k_stride_h;
+  a.sh[1] = v_stride_h;
+  a.n = n;
+  a.slots = reinterpret_cast<const long long*>(slots);
+  a.cache[0] = k_cache;
+  a.cache[1] = v_cache;
+  a.scale[0] = k_scale;
+  a.scale[1] = v_scale;
+  a.num_blocks = num_blocks;
+  a.bs_log = log2_of(block_size);
+  a.H = kv_heads;
+  a.status = dev_status;
+  // as many rows a warp as leave 32 warps for every SM
+  const int64_t want = (int64_t)sm_count() * 32;
+  int64_t rpw = n * kv_heads * 2 / want;
+  a.rows_per_warp = (int)(rpw < 1 ? 1 : rpw > 32 ? 32 : rpw);
+  const cudaStream_t st = S(stream);
+  return dtype == MPZCH_F32 ? launch_append_dim<float>(a, dim, st)
+                            : dtype == MPZCH_F16 ? launch_append_dim<__half>(a, dim, st)
+                                                 : launch_append_dim<__nv_bfloat16>(a, dim, st);
+}
+
+int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim) {
+  if (kv_heads < 1 || q_heads < 1 || q_heads > 4096 || q_heads % kv_heads || !dim_ok(dim)) return -1;
+  return part_bytes(dim);
+}
+
+int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64_t n, int32_t dtype,
+                    const int8_t* k_cache, const int8_t* v_cache, const float* k_scale,
+                    const float* v_scale, int64_t num_blocks, int32_t block_size, int32_t q_heads,
+                    int32_t kv_heads, int32_t dim, const int32_t* block_table, int32_t max_blocks,
+                    const int32_t* cu_new, const int32_t* seq_len, int32_t n_requests,
+                    int32_t max_new, float softmax_scale, int32_t causal, int32_t window, void* out,
+                    int64_t out_stride_n, int64_t out_stride_h, float* lse, void* workspace,
+                    int64_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const int bytes = type_bytes(dtype);
+  const int64_t need = mpzch_kv_attend_workspace(q_heads, kv_heads, dim);
+  if (need < 0 || bytes == 0 || n < 0 || n > kMaxInt || !block_size_ok(block_size) ||
+      num_blocks < 0 || num_blocks > kMaxInt || max_blocks < 0 || n_requests < 0 ||
+      n_requests > MPZCH_KV_MAX_REQUESTS || max_new < 0 || !std::isfinite(softmax_scale) ||
+      window < 0 || (window > 0 && !causal) ||
+      ((int64_t)max_blocks * block_size > kMaxInt))
+    return MPZCH_EINVAL;
+  if (n == 0 || n_requests == 0) return MPZCH_OK;
+  if (!q || !out || !cu_new || !seq_len || (max_blocks > 0 && !block_table) ||
+      (num_blocks > 0 && (!k_cache || !v_cache || !k_scale || !v_scale)) || !workspace ||
+      workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+      !rows_ok(q, q_stride_n, q_stride_h, bytes) || !rows_ok(out, out_stride_n, out_stride_h, bytes) ||
+      !aligned16(k_cache) || !aligned16(v_cache))
+    return MPZCH_EINVAL;
+  AttendArgs a;
+  a.q = q;
+  a.qsn = q_stride_n;
+  a.qsh = q_stride_h;
+  a.n = n;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.num_blocks = num_blocks;
+  a.bs_log = log2_of(block_size);
+  a.Hq = q_heads;
+  a.H = kv_heads;
+  a.G = q_heads / kv_heads;
+  a.table = block_table;
+  a.max_blocks = max_blocks;
+  a.cu = cu_new;
+  a.seq = seq_len;
+  a.B = n_requests;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.causal = causal ? 1 : 0;
+  a.window = window;
+  a.out = out;
+  a.osn = out_stride_n;
+  a.osh = out_stride_h;
+  a.lse = lse;
+  a.status = dev_status;
+  a.most_rows = INT64_MAX;
+  a.min_steps = 4;
+  a.heads = static_cast<PartHead*>(workspace);
+  a.parts = reinterpret_cast<float*>(
+      static_cast<char*>(workspace) +
+      ((int64_t)row_grid_blocks() * (int64_t)sizeof(PartHead) + 255) / 256 * 256);
+  const cudaStream_t st = S(stream);
+  return dtype == MPZCH_F32 ? launch_rows_dim<float, 2, 2>(a, dim, st)
+                            : dtype == MPZCH_F16 ? launch_rows_dim<__half, 1, 2>(a, dim, st)
+                                                 : launch_rows_dim<__nv_bfloat16, 1, 1>(a, dim, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,385 @@
+// Device code of the history cache: block tables and slots, the int8 append,
+// and attention for few rows per request (include/mpzch.h, "History cache").
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "mpzch_device.cuh"
+
+namespace mpzch_kv {
+
+using namespace mpzch;
+
+constexpr int kStBadLen = 32, kStNoBlock = 64, kStBadBlock = 128;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// ---------------------------------------------------------------------------
+// Block tables and slots.
+// ---------------------------------------------------------------------------
+struct TablesArgs {
+  const int32_t *cached, *news;
+  int B, bs_log;
+  const int32_t* free_blocks;
+  int64_t n_free;
+  const long long* free_count;
+  int32_t* table;
+  int max_blocks;
+  int32_t *cu, *seq;
+  long long* slots;
+  int64_t n_slots;
+  long long* free_out;
+  int32_t* status;
+};
+
+// Inclusive scan of one value per thread over the block; `total` gets the sum.
+__device__ __forceinline__ long long block_scan(long long x, long long* s_warp, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(kAll, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();  // s_warp may still be read from the previous scan
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  long long before = 0, sum = 0;
+  long long w = lane < nw ? s_warp[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(kAll, w, d);
+    if (lane >= d) w += y;
+  }
+  before = __shfl_sync(kAll, w, (warp + 31) & 31);
+  sum = __shfl_sync(kAll, w, 31);
+  total = sum;
+  return x + (warp ? before : 0);
+}
+
+// First index in the non-decreasing s[0..n) whose value is > x (n if none).
+__device__ __forceinline__ int first_above(const int32_t* s, int n, int x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (s[mid] > x)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// One launch.  Every block scans all requests (at most 16,384: two ints each,
+// from L2) into shared memory and then writes its share of the rows, of the new
+// table entries and of the lengths, so no block waits for another.
+__global__ void __launch_bounds__(1024) k_kv_tables(TablesArgs a) {
+  pdl_enter();
+  extern __shared__ int32_t s_dyn[];
+  __shared__ long long s_warp[32];
+  int32_t* s_end = s_dyn;          // rows up to and with request b
+  int32_t* s_upto = s_dyn + a.B;   // blocks needed up to and with request b
+  constexpr long long kTop = 0x7FFFFFFFll;
+  const int bs = 1 << a.bs_log, tid = threadIdx.x, nt = blockDim.x;
+  long long count = *a.free_count;
+  count = count < 0 ? 0 : count > a.n_free ? a.n_free : count;
+  long long tok0 = 0, need0 = 0;
+  int bits = 0;
+  for (int base = 0; base < a.B; base += nt * 4) {
+    const int b0 = base + tid * 4;
+    long long c[4], w[4], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = b0 + i < a.B;
+      c[i] = in ? a.cached[b0 + i] : 0;
+      w[i] = in ? a.news[b0 + i] : 0;
+      sum += w[i] > 0 ? w[i] : 0;
+    }
+    long long end = block_scan(sum, s_warp, total) - sum + tok0;
+    tok0 += total;
+    long long need[4];
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      end += w[i] > 0 ? w[i] : 0;
+      const long long all = (c[i] + w[i] + bs - 1) >> a.bs_log;
+      const bool bad = c[i] < 0 || w[i] < 0 || all > a.max_blocks || end > a.n_slots;
+      if (bad) bits |= kStBadLen;
+      need[i] = bad ? 0 : all - ((c[i] + bs - 1) >> a.bs_log);
+      sum += need[i];
+      if (b0 + i < a.B) s_end[b0 + i] = (int32_t)(end < kTop ? end : kTop);
+    }
+    long long upto = block_scan(sum, s_warp, total) - sum + need0;
+    need0 += total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      upto += need[i];
+      if (need[i] > 0 && upto > count) bits |= kStNoBlock;
+      if (b0 + i < a.B) s_upto[b0 + i] = (int32_t)(upto < kTop ? upto : kTop);
+    }
+  }
+  __syncthreads();
+  const int gtid = blockIdx.x * nt + tid, gthreads = gridDim.x * nt;
+  // blocks given out: the largest s_upto that the list holds
+  const int served = first_above(s_upto, a.B, (int)count);
+  const int given = served ? s_upto[served - 1] : 0;
+  if (blockIdx.x == 0) {
+    if (bits) set_status(a.status, bits);
+    if (tid == 0) {
+      a.cu[0] = 0;
+      *a.free_out = count - given;
+    }
+  }
+  // lengths
+  for (int b = gtid; b < a.B; b += gthreads) {
+    const long long c = a.cached[b], w = a.news[b];
+    const long long all = (c + w + bs - 1) >> a.bs_log;
+    const bool bad = c < 0 || w < 0 || all > a.max_blocks || s_end[b] > a.n_slots;
+    const int32_t before = b ? s_upto[b - 1] : 0;
+    const bool ok = !bad && (s_upto[b] == before || s_upto[b] <= count);
+    a.cu[b + 1] = s_end[b];
+    a.seq[b] = (int32_t)(ok ? c + w : c > 0 ? c : 0);
+  }
+  // new table entries: entry e of those given out belongs to the first request
+  // with s_upto > e
+  for (int e = gtid; e < given; e += gthreads) {
+    const int b = first_above(s_upto, served, e);
+    const int before = b ? s_upto[b - 1] : 0;
+    const long long old = ((long long)a.cached[b] + bs - 1) >> a.bs_log;
+    a.table[(int64_t)b * a.max_blocks + old + (e - before)] = a.free_blocks[count - 1 - e];
+  }
+  // slots, 4 rows a thread
+  const int64_t rows = tok0 < a.n_slots ? tok0 : a.n_slots;
+  for (int64_t i0 = (int64_t)gtid * 4; i0 < a.n_slots; i0 += (int64_t)gthreads * 4) {
+    long long out[4] = {-1, -1, -1, -1};
+    if (i0 < rows) {
+      int b = first_above(s_end, a.B, (int)i0);
+      bool ok = false;
+      long long c = 0, start = 0, old = 0, held = -1;
+      int32_t before = 0, next = 0;
+      bool fresh = true;
+      long long blk = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = i0 + i;
+        if (r < rows) {
+          while (r >= s_end[b]) {
+            ++b;
+            fresh = true;
+          }
+          if (fresh) {
+            c = a.cached[b];
+            start = b ? s_end[b - 1] : 0;
+            old = (c + bs - 1) >> a.bs_log;
+            before = b ? s_upto[b - 1] : 0;
+            next = s_upto[b];
+            const long long all = (c + (s_end[b] - start) + bs - 1) >> a.bs_log;
+            ok = c >= 0 && all <= a.max_blocks && s_end[b] <= a.n_slots &&
+                 (next == before || next <= count);
+            held = -1;
+            fresh = false;
+          }
+          if (ok) {
+            const long long pos = c + (r - start), j = pos >> a.bs_log;
+            if (j != held) {
+              blk = j < old ? a.table[(int64_t)b * a.max_blocks + j]
+                            : a.free_blocks[count - 1 - (before + (j - old))];
+              held = j;
+            }
+            out[i] = (blk << a.bs_log) + (pos & (bs - 1));
+          }
+        }
+      }
+    }
+    if (i0 + 4 <= a.n_slots && (reinterpret_cast<uintptr_t>(a.slots) & 15) == 0) {
+      reinterpret_cast<longlong2*>(a.slots + i0)[0] = make_longlong2(out[0], out[1]);
+      reinterpret_cast<longlong2*>(a.slots + i0)[1] = make_longlong2(out[2], out[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < a.n_slots) a.slots[i0 + i] = out[i];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Append.
+// ---------------------------------------------------------------------------
+struct AppendArgs {
+  const void* x[2];        // k, v
+  int64_t sn[2], sh[2];    // element strides of rows and heads
+  int64_t n;
+  const long long* slots;
+  int8_t* cache[2];
+  float* scale[2];
+  int64_t num_blocks;
+  int bs_log, H;
+  int rows_per_warp;       // 1..32
+  int32_t* status;
+};
+
+// 16 consecutive values as fp32.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&x)[16]);
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    x[4 * i] = v.x;
+    x[4 * i + 1] = v.y;
+    x[4 * i + 2] = v.z;
+    x[4 * i + 3] = v.w;
+  }
+}
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+}
+template <>
+__device__ __forceinline__ void load16<__half>(const __half* p, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __half2 h;
+      *reinterpret_cast<uint32_t*>(&h) = w[j];
+      const float2 f = __half22float2(h);
+      x[8 * i + 2 * j] = f.x;
+      x[8 * i + 2 * j + 1] = f.y;
+    }
+  }
+}
+
+// max of |x| as bit patterns: for non-negative floats the order of the bits is
+// the order of the values, with every NaN above infinity.
+__device__ __forceinline__ uint32_t absmax16(const float (&x)[16], uint32_t a) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    a = b > a ? b : a;
+  }
+  return a;
+}
+
+__device__ __forceinline__ uint4 codes16(const float (&x)[16], float s, float rcp, bool usable) {
+  int t[16];
+  if (usable) {
+    quant_lane<16>(x, s, rcp, isfinite(rcp), t);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = 0;
+  }
+  return make_uint4(pack4(t[0], t[1], t[2], t[3]), pack4(t[4], t[5], t[6], t[7]),
+                    pack4(t[8], t[9], t[10], t[11]), pack4(t[12], t[13], t[14], t[15]));
+}
+
+// One warp takes rows_per_warp rows of the batch for one head of one cache and
+// works through the runs that begin there.  A lane handles 16 values of a token:
+// 32 * 16 / D tokens a pass.  Values of the first kKeep passes stay in
+// registers between the maximum and the codes; longer runs are read again.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_kv_append(AppendArgs a) {
+  pdl_enter();
+  constexpr int kLanes = D / 16, kTok = 32 / kLanes, kKeep = 4;
+  const int lane = threadIdx.x & 31, bs = 1 << a.bs_log;
+  const int sub = lane % kLanes, tok = lane / kLanes;
+  const int64_t tasks = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2;
+  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  for (int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; task < tasks;
+       task += warps) {
+    const int h = (int)(task % a.H);
+    const int which = (int)(task / a.H % 2);
+    const int64_t row0 = task / a.H / 2 * a.rows_per_warp;
+    const T* __restrict__ src = static_cast<const T*>(which ? a.x[1] : a.x[0]);
+    const int64_t sn = which ? a.sn[1] : a.sn[0], sh = which ? a.sh[1] : a.sh[0];
+    int8_t* cache = which ? a.cache[1] : a.cache[0];
+    float* scale = which ? a.scale[1] : a.scale[0];
+    const int64_t mine = row0 + lane;
+    const bool in = lane < a.rows_per_warp && mine < a.n;
+    const long long slot_l = in ? a.slots[mine] : -1;
+    const long long prev_l = in && mine > 0 ? a.slots[mine - 1] : -2;
+    const bool bad = slot_l >= 0 && (slot_l >> a.bs_log) >= a.num_blocks;
+    if (bad) set_status(a.status, kStBadBlock);
+    unsigned heads = __ballot_sync(
+        kAll, slot_l >= 0 && !bad && (slot_l != prev_l + 1 || (slot_l & (bs - 1)) == 0));
+    while (heads) {
+      const int l = __ffs(heads) - 1;
+      heads &= heads - 1;
+      const long long slot = __shfl_sync(kAll, slot_l, l);
+      const int64_t row = row0 + l, blk = slot >> a.bs_log;
+      const int o = (int)(slot & (bs - 1));
+      int len = 0;
+      for (int d = 0; d < bs - o; d += 32) {
+        const bool next = d + lane < bs - o && row + d + lane < a.n &&
+                          a.slots[row + d + lane] == slot + d + lane;
+        const unsigned miss = ~__ballot_sync(kAll, next);
+        len += miss ? __ffs(miss) - 1 : 32;
+        if (miss) break;
+      }
+      const T* p = src + row * sn + h * sh + sub * 16;
+      float x[kKeep][16];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (i * kTok + tok < len) {
+          load16<T>(p + (int64_t)(i * kTok + tok) * sn, x[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (i * kTok + tok < len) amax = absmax16(x[i], amax);
+      for (int i = kKeep * kTok + tok; i < len; i += kTok) {
+        float y[16];
+        load16<T>(p + (int64_t)i * sn, y);
+        amax = absmax16(y, amax);
+      }
+      amax = __reduce_max_sync(kAll, amax);
+      float* sp = scale + blk * a.H + h;
+      const float before = o > 0 ? *sp : 0.f;
+      const float own = __fdiv_rn(__uint_as_float(amax), 127.0f);
+      // the larger one; a NaN on either side stays
+      const float s = own != own ? own : (before >= own || before != before) ? before : own;
+      const bool usable = s > 0.f && s < CUDART_INF_F;
+      const float rcp = usable ? __frcp_rn(s) : 0.f;
+      int8_t* base = cache + (blk * a.H + h) * ((int64_t)bs * D) + sub * 16;
+      if (o > 0 && s != before && (s == s || before == before)) {
+        for (int i = tok; i < o; i += kTok) {
+          uint4* c = reinterpret_cast<uint4*>(base + (int64_t)i * D);
+          const uint4 v = *c;
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          float y[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            y[j] = __fmul_rn((float)(int8_t)(w[j / 4] >> (8 * (j % 4))), before);
+          *c = codes16(y, s, rcp, usable);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (i * kTok + tok < len)
+          *reinterpret_cast<uint4*>(base + (int64_t)(o + i * kTok + tok) * D) =
+              codes16(x[i], s, rcp, usable);
+      for (int i = kKeep * kTok + tok; i < len; i += kTok) {
+        float y[16];
+        load16<T>(p + (int64_t)i * sn, y);
+        *reinterpret_cast<uint4*>(base + (int64_t)(o + i) * D) = codes16(y, s, rcp, usable);
+      }
+      __syncwarp();
+      if (lane == 0) *sp = s;
+    }
+  }
+}
+
+}  // namespace mpzch_kv

@@ -72,6 +72,9 @@ extern "C" {
 #define MPZCH_STATUS_BADAO 4    /* an always-on row outside [0, ao_nrows) was given */
 #define MPZCH_STATUS_INTERNAL 8 /* an internal bound was hit (never expected) */
 #define MPZCH_STATUS_TIMEOUT 16 /* a bulk row copy did not complete within its time limit */
+#define MPZCH_STATUS_BADLEN 32   /* a request length, or its place in the batch, was refused */
+#define MPZCH_STATUS_NOBLOCK 64  /* the list of free blocks did not last for every request */
+#define MPZCH_STATUS_BADBLOCK 128 /* a block id or slot outside the history cache was given */
 
 typedef struct mpzch_table mpzch_table;
 
@@ -258,6 +261,107 @@ MPZCH_API int mpzch_serve_gather(const int64_t* snap_keys, int64_t capacity, int
                        const int8_t* snap_q, const float* snap_scale, int32_t dim,
                        const int64_t* ids, int64_t n, int32_t* rows, uint8_t* hit, float* out,
                        int32_t* dev_status, void* stream);
+
+/* ---- History cache ----------------------------------------------------------
+ * The serving read's counterpart for sequence models: the tokens of a request's
+ * history are kept as int8 codes under the export's rule, and later tokens (or
+ * candidates) attend over them.  The cache is blocks of block_size tokens:
+ *   k_cache, v_cache  device int8 [num_blocks][kv_heads][block_size][dim]
+ *   k_scale, v_scale  device fp32 [num_blocks][kv_heads]   (code * scale = value)
+ * block_size: 16, 32, 64 or 128; dim: 32, 64 or 128.  A block belongs to one
+ * request and is filled from its first token on.  Slot of a token:
+ * block * block_size + offset.  A batch of new tokens is ragged: the rows of
+ * request b are cu_new[b] .. cu_new[b + 1] - 1.
+ *
+ * None of these calls takes a table handle, allocates, or waits for the device;
+ * they can be captured into a graph, and run on any device that is current and
+ * owns all of the call's buffers.  dev_status: nullable device int32, OR-ed with
+ * MPZCH_STATUS_* bits.  Buffers of one call must not overlap unless stated. */
+#define MPZCH_F32 0
+#define MPZCH_F16 1
+#define MPZCH_BF16 2
+#define MPZCH_KV_MAX_REQUESTS 16384
+
+/* Block tables and slots from request lengths.  With c = cached_len[b] tokens
+ * held, w = new_len[b] tokens to come and S = block_size, request b needs
+ *   need_b = ceil((c + w) / S) - ceil(c / S)   new blocks, P_b = need_0 + .. + need_b.
+ * A request is refused, with MPZCH_STATUS_BADLEN, for a negative length, for more
+ * than max_blocks blocks, or when its rows pass n_slots; it then needs none.  Any
+ * other one with need_b > 0 and P_b > *free_count is refused with
+ * MPZCH_STATUS_NOBLOCK (so requests are served in order).  Then
+ *   cu_new[b]    = sum of max(new_len, 0) before b, at most 2^31 - 1   (int32[B + 1])
+ *   seq_len[b]   = c + w, or max(c, 0) when refused                    (int32[B])
+ *   block_table[b][ceil(c/S) + j] = free_blocks[*free_count - 1 - (P_b - need_b + j)],
+ *                  j < need_b; no other entry is written               (int32[B][max_blocks])
+ *   slots[cu_new[b] + t] = slot of token c + t, or -1 when refused; rows from
+ *                  cu_new[B] to n_slots - 1: -1                        (int64[n_slots])
+ *   *free_count_out = *free_count less the blocks given out (taken from the end of
+ *                  the list; given-back blocks are appended there).
+ * cached_len, new_len: device int32[B], B = n_requests <= MPZCH_KV_MAX_REQUESTS;
+ * free_blocks: device int32[n_free_blocks]; free_count: device int64, taken as
+ * at most n_free_blocks.  The outputs must not alias the inputs. */
+MPZCH_API int mpzch_kv_tables(const int32_t* cached_len, const int32_t* new_len, int32_t n_requests,
+                              int32_t block_size, const int32_t* free_blocks, int64_t n_free_blocks,
+                              const int64_t* free_count, int32_t* block_table, int32_t max_blocks,
+                              int32_t* cu_new, int32_t* seq_len, int64_t* slots, int64_t n_slots,
+                              int64_t* free_count_out, int32_t* dev_status, void* stream);
+
+/* Appends the keys and values of n tokens to their blocks.  k, v: device
+ * [n][kv_heads][dim] of type dtype (MPZCH_F32, MPZCH_F16, MPZCH_BF16), values of a
+ * head contiguous, rows k_stride_n / v_stride_n and heads k_stride_h / v_stride_h
+ * elements apart (every head must start on a 16-byte boundary).  slots: device
+ * int64[n].  A run is a maximal sequence of rows with consecutive slots of one
+ * block; its first offset o says how many tokens the block holds already.  For
+ * each run, head and cache, with a = max|x| over the run's values:
+ *   s = max(o > 0 ? old scale : 0, a / 127)     (binary32; NaN if either is)
+ *   tokens before o, when s differs from the old scale (two NaN do not):
+ *                       q = clamp(rne(fl(q * old) / s))
+ *   the run's tokens: q = clamp(rne(x / s));  s == 0, infinite or NaN gives q = 0.
+ * This is the export's rule with the block as its row; a scale never shrinks.
+ * Rows with a negative slot are skipped (padding, refused requests); a slot past
+ * the cache is skipped with MPZCH_STATUS_BADBLOCK.  Only one run of a call may
+ * fall into a block: with more, that block's content is undefined (nothing else
+ * is). */
+MPZCH_API int mpzch_kv_append(const void* k, int64_t k_stride_n, int64_t k_stride_h, const void* v,
+                              int64_t v_stride_n, int64_t v_stride_h, int64_t n, int32_t dtype,
+                              const int64_t* slots, int8_t* k_cache, int8_t* v_cache,
+                              float* k_scale, float* v_scale, int64_t num_blocks,
+                              int32_t block_size, int32_t kv_heads, int32_t dim,
+                              int32_t* dev_status, void* stream);
+
+/* Bytes of device workspace that mpzch_kv_attend needs, or -1 for bad sizes. */
+MPZCH_API int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, int32_t dim);
+
+/* Attention of the batch's rows over the cached histories.  Row t (of w) of
+ * request b, query head h, with L = seq_len[b] and position p = L - w + t:
+ *   out = sum_j softmax_j(softmax_scale * <q, k_j>) v_j over the keys j of b with
+ *   j < L;  causal: j <= p;  window > 0 (needs causal): j > p - window,
+ * k_j, v_j the values (code * scale) of kv head h / (q_heads / kv_heads).  A row
+ * that sees no key gives out = 0, lse = -inf.  lse: nullable device fp32
+ * [n][q_heads], natural logarithm of the softmax's denominator.  q, out: device
+ * [n][q_heads][dim] of type dtype, strides in elements as for mpzch_kv_append.
+ * Rows from cu_new[B] on are neither read nor written.  max_new: the caller's
+ * bound on a request's rows; it chooses kernels and changes no result.
+ * Key positions come through block_table (int32[B][max_blocks]); a block id
+ * outside the cache hides its keys (MPZCH_STATUS_BADBLOCK), a length past
+ * max_blocks * block_size or a cu_new outside 0..n is cut (MPZCH_STATUS_BADLEN).
+ * Arithmetic: scores, maxima, sums and accumulators in fp32.  Products take
+ * fp16 operands, the codes exactly and the queries after a power-of-two scaling of
+ * the row (F32: in two parts, 22 bits); softmax weights are rounded to fp16
+ * (F32: two parts).  A query row with a NaN or an infinity that sees a key gives
+ * NaN.  Results do not depend on timing (no float atomics).
+ * workspace: device, 256-byte aligned, mpzch_kv_attend_workspace bytes; calls
+ * that may overlap on the device need one each. */
+MPZCH_API int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64_t n,
+                              int32_t dtype, const int8_t* k_cache, const int8_t* v_cache,
+                              const float* k_scale, const float* v_scale, int64_t num_blocks,
+                              int32_t block_size, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                              const int32_t* block_table, int32_t max_blocks,
+                              const int32_t* cu_new, const int32_t* seq_len, int32_t n_requests,
+                              int32_t max_new, float softmax_scale, int32_t causal, int32_t window,
+                              void* out, int64_t out_stride_n, int64_t out_stride_h, float* lse,
+                              void* workspace, int64_t workspace_bytes, int32_t* dev_status,
+                              void* stream);
 
 /* ---- Hash-owner sharding --------------------------------------------------
  * Memory Layer section 2 shards the table across devices and keeps the
