@@ -47,23 +47,37 @@ int launch_append_dim(const AppendArgs& a, int dim, cudaStream_t st) {
                    : dim == 64 ? launch_append<T, 64>(a, st) : launch_append<T, 128>(a, st);
 }
 
-int row_grid_blocks() { return sm_count() * kRowBlocksPerSm; }
+int row_workers() { return sm_count() * kRowBlocksPerSm * kRowWarps; }
 
-int64_t part_bytes(int dim) {
-  const int64_t blocks = row_grid_blocks();
-  const int64_t heads = (blocks * (int64_t)sizeof(PartHead) + 255) / 256 * 256;
-  return heads + blocks * 2 * kRowTile * (dim + 2) * (int64_t)sizeof(float);
+int64_t head_bytes() {
+  return (row_workers() * (int64_t)sizeof(PartHead) + 255) / 256 * 256;
 }
 
-template <int D, typename T, int NQ, int NP>
+int64_t part_bytes(int dim) {
+  return head_bytes() + row_workers() * 2ll * kMaxRows * (dim + 2) * (int64_t)sizeof(float);
+}
+
+template <int D, typename T, int R, int NQ, int NP>
 int launch_rows(const AttendArgs& a, cudaStream_t st) {
-  const void* kern = reinterpret_cast<const void*>(k_kv_rows<D, T, NQ, NP>);
-  int per_sm = resident_blocks(kern, 32 * kRowWarps, 0);
+  const void* kern = reinterpret_cast<const void*>(k_kv_rows<D, T, R, NQ, NP>);
+  int rc = allow_dynamic_smem(kern, row_smem(D));
+  if (rc) return rc;
+  int per_sm = resident_blocks(kern, 32 * kRowWarps, row_smem(D));
   if (per_sm > kRowBlocksPerSm) per_sm = kRowBlocksPerSm;
   const unsigned grid = (unsigned)(sm_count() * per_sm);
-  int rc = launch(k_kv_rows<D, T, NQ, NP>, grid, 32 * kRowWarps, st, true, a);
-  if (!rc) rc = launch(k_kv_join<D, T>, grid, 256, st, true, a);
+  rc = launch_smem(k_kv_rows<D, T, R, NQ, NP>, grid, 32 * kRowWarps, row_smem(D), st, true, a);
+  const int64_t rows = (int64_t)a.max_new * a.G;
+  const int y = rows < 1 ? 1 : rows < 4 ? (int)rows : 4;
+  if (!rc)
+    rc = launch(k_kv_join<D, T, R>, dim3(grid * kRowWarps, y), 32 * kJoinWarps, st, true, a);
   return rc;
+}
+
+// Tiles of 8 rows where no request has more, else of 16.
+template <int D, typename T, int NQ, int NP>
+int launch_rows(const AttendArgs& a, cudaStream_t st) {
+  return (int64_t)a.max_new * a.G <= 8 ? launch_rows<D, T, 8, NQ, NP>(a, st)
+                                       : launch_rows<D, T, 16, NQ, NP>(a, st);
 }
 
 template <typename T, int NQ, int NP>
@@ -175,7 +189,7 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
       num_blocks < 0 || num_blocks > kMaxInt || max_blocks < 0 || n_requests < 0 ||
       n_requests > MPZCH_KV_MAX_REQUESTS || max_new < 0 || !std::isfinite(softmax_scale) ||
       window < 0 || (window > 0 && !causal) ||
-      ((int64_t)max_blocks * block_size > kMaxInt))
+      ((int64_t)max_blocks * block_size > kMaxInt - 1024))
     return MPZCH_EINVAL;
   if (n == 0 || n_requests == 0) return MPZCH_OK;
   if (!q || !out || !cu_new || !seq_len || (max_blocks > 0 && !block_table) ||
@@ -212,11 +226,10 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
   a.lse = lse;
   a.status = dev_status;
   a.most_rows = INT64_MAX;
-  a.min_steps = 4;
+  a.min_units = 1;
+  a.max_new = max_new;
   a.heads = static_cast<PartHead*>(workspace);
-  a.parts = reinterpret_cast<float*>(
-      static_cast<char*>(workspace) +
-      ((int64_t)row_grid_blocks() * (int64_t)sizeof(PartHead) + 255) / 256 * 256);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + head_bytes());
   const cudaStream_t st = S(stream);
   return dtype == MPZCH_F32 ? launch_rows_dim<float, 2, 2>(a, dim, st)
                             : dtype == MPZCH_F16 ? launch_rows_dim<__half, 1, 2>(a, dim, st)

@@ -5,9 +5,10 @@
 
 namespace mpzch_kv {
 
-constexpr int kRowTile = 16;    // query rows (token, head of the group) of one tile
-constexpr int kStepKeys = 64;   // keys of one step of a block: 16 for each of 4 warps
-constexpr int kRowWarps = 4;
+constexpr int kMaxRows = 16;    // query rows (token, head of the group) of a tile: 8 or 16
+constexpr int kUnitKeys = 64;   // keys of one unit of work: four steps of a warp
+constexpr int kStepKeys = 16;
+constexpr int kRowWarps = 4;    // independent warps of a block
 constexpr int kRowBlocksPerSm = 4;
 
 struct AttendArgs {
@@ -28,13 +29,14 @@ struct AttendArgs {
   float* lse;
   int32_t* status;
   int64_t most_rows;  // requests with more rows are left to the tile kernel
-  int min_steps;      // steps that a block takes at least
+  int min_units;      // units that a warp takes at least
+  int max_new;        // the caller's bound on a request's rows: sizes the join's grid
   struct PartHead* heads;
-  float* parts;       // [block][2][kRowTile][D + 2]
+  float* parts;       // [warp][2]: [R][D] outputs, [R][2] maxima and sums
 };
 
-// What a block of k_kv_rows leaves for k_kv_join: the item that begins in the
-// block and ends in block `last` (< 0: none).
+// What a warp of k_kv_rows leaves for k_kv_join: the item that begins in the
+// warp's share and ends in that of warp `last` (< 0: none).
 struct PartHead {
   int32_t b, h, tile, last;
 };
@@ -66,19 +68,21 @@ __device__ __forceinline__ int64_t first_key(const AttendArgs& a, const Request&
   return lo > 0 ? lo & ~(int64_t)15 : 0;
 }
 
-// Steps of one (head, row tile) of the request; every such item has the same
+// Units of one (head, row tile) of the request; every such item has the same
 // number, at least one.
-__device__ __forceinline__ int64_t item_steps(const AttendArgs& a, const Request& r) {
+__device__ __forceinline__ int64_t item_units(const AttendArgs& a, const Request& r) {
   const int64_t keys = r.L - first_key(a, r);
-  return keys > kStepKeys ? (keys + kStepKeys - 1) / kStepKeys : 1;
+  return keys > kUnitKeys ? (keys + kUnitKeys - 1) / kUnitKeys : 1;
 }
 
+template <int R>
 __device__ __forceinline__ int64_t row_tiles(const AttendArgs& a, const Request& r) {
-  return r.w * a.G > a.most_rows ? 0 : (r.w * a.G + kRowTile - 1) / kRowTile;
+  return r.w * a.G > a.most_rows ? 0 : (r.w * a.G + R - 1) / R;
 }
 
+template <int R>
 __device__ __forceinline__ int64_t request_units(const AttendArgs& a, const Request& r) {
-  return row_tiles(a, r) * a.H * item_steps(a, r);
+  return row_tiles<R>(a, r) * a.H * item_units(a, r);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -100,6 +104,13 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 8 x 8 matrix of fp16, a row to four lanes, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Codes (biased by 128) of bytes `sel` of x as two fp16 numbers: 0x6400 | u is
 // 1024 + u exactly, and 1152 = 1024 + 128 comes off exactly.
 __device__ __forceinline__ uint32_t codes_half2(uint32_t biased, uint32_t sel) {
@@ -111,22 +122,41 @@ __device__ __forceinline__ uint32_t codes_half2(uint32_t biased, uint32_t sel) {
 constexpr uint32_t kSelLow = 0x4140, kSelHigh = 0x4342;
 
 template <int kWords>
-struct Words {
-  uint32_t w[kWords];
-};
-
-// kWords 32-bit words of the cache, past L1 (every byte is read once).
-template <int kWords>
-__device__ __forceinline__ void load_words(const int8_t* p, uint32_t* w) {
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
   if constexpr (kWords == 4) {
-    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-        : "l"(p));
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
   } else if constexpr (kWords == 2) {
-    asm("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
   } else {
-    asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
   }
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const int8_t* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Byte of 16-byte chunk `col` of row `row` in a staged 16 x D tile.  The rows lie
+// one behind the other; chunks change places within a 128-byte line so that the
+// lanes of one shared-memory phase hit different banks:
+//  keys, D = 128: lanes (row r, chunk c) of two rows r, r + 1 meet: bit 2 by r's parity
+//  values: lanes (row 2c, chunk of r) of four even (or odd) rows meet.
+template <int D, bool kValue>
+__device__ __forceinline__ int staged(int row, int col) {
+  const int at = row * (D / 16) + col, line = at >> 3, p = at & 7;
+  if constexpr (!kValue)
+    return D == 128 ? line * 128 + ((p ^ ((row & 1) << 2)) << 4) : at << 4;
+  const int x = D == 128 ? row & 7 : D == 64 ? (2 * line) & 7 : (2 * line) & 2;
+  return line * 128 + ((p ^ x) << 4);
 }
 
 // 4 consecutive query values as fp32.
@@ -164,107 +194,206 @@ __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// State of one warp for one item: rows r and r + 8 of the tile, r = lane / 4.
-template <int D>
-struct RowState {
-  float acc[D / 8][4];
-  float m[2], l[2];  // running maximum (log2 units) and sum of this lane's columns
-  float vref;        // power of two at or above the value scales seen
-};
-
 // The softmax weights are kept as p * 2^7 * (value scale / vref) in fp16: p is at
 // most 2^kSlack (the maximum is moved only when a score passes it by more than
-// that), so the largest is 2^15, and weights down to 2^-29 of it keep 11 bits.
+// that), so the largest is 2^15; weights below 2^-21 of the largest lose bits and
+// those below 2^-32 vanish.
 constexpr float kSlack = 8.f;
 constexpr float kWeightScale = 128.f;
 
-// Rows by 16 keys of one warp.  Q row fragments: lane (r, c), c = lane % 4, holds
-// for k-step kk the dims of word kk of the key bytes that the lane itself loads,
-// so no byte changes lanes: a key row's chunk of 64 dims is 4 lanes x 16 bytes.
-template <int D, typename T, int NQ, int NP>
-__global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 && D <= 64 ? 3 : 2) k_kv_rows(AttendArgs a) {
+// 16-key slots of a warp's ring: one being read, the others in flight.  16 KB a warp
+// at D = 128: 12 warps of an SM have 144 KB under way.
+__host__ __device__ constexpr int row_slots(int D) { return D == 128 ? 4 : D == 64 ? 5 : 8; }
+__host__ __device__ constexpr int row_smem(int D) { return kRowWarps * row_slots(D) * 2 * kStepKeys * D; }
+
+// Writes D / 8 consecutive outputs.
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* p, const float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+    store4<T>(p + i, y);
+  }
+}
+
+// Single tokens and other few rows.  Every warp is a worker of its own: the units
+// (64 keys of one request, kv head and row tile) of the whole batch are laid in a
+// row and each warp takes an equal share of them, so ragged histories balance
+// without the host knowing a length.  An item that two shares cut leaves parts for
+// k_kv_join.  A warp works 16 keys of one block at a time while cp.async brings the
+// next ones (a ring per warp, no block-wide barrier).  Products are m16n8k16 in fp16,
+// the codes turned into fp16 in registers as operand A (16 rows of it), the few query
+// rows as the 8-wide operand B:
+//   scores   S^T = K Q^T      A: 16 keys x 16 dims
+//   outputs  O^T = V^T P^T    A: 16 dims x 16 keys; P^T is S^T's lanes transposed
+//                             (movmatrix on pairs of fp16)
+// so 8 rows need half of what a 16-row tile of queries as A would.  Dims and keys are
+// assigned to lanes so that no code changes lanes: for keys, lane (r, c) holds chunks c
+// of keys r and r + 8 (dims in the same order for the queries); for values it holds
+// keys 2c, 2c+1, 2c+8, 2c+9 and D / 8 neighbouring dims, two to each 16-dim tile.
+template <int D, typename T, int R, int NQ, int NP>
+__global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : NQ == 1 ? 3 : 2)
+    k_kv_rows(AttendArgs a) {
   pdl_enter();
   constexpr int kWK = D >= 64 ? 4 : 2;       // words per load of key bytes
   constexpr int kChunks = D >= 64 ? D / 64 : 1;
   constexpr int kK = kWK * kChunks;          // key words a lane holds per key = MMA k-steps
   constexpr int kWV = D / 32;                // value words a lane holds per key
-  constexpr int kRow = D + 4;                // row pitch of the join in shared memory
-  __shared__ __align__(16) float s_acc[kRowWarps][kRowTile][kRow];
-  __shared__ float s_m[kRowWarps][kRowTile], s_l[kRowWarps][kRowTile], s_v[kRowWarps];
+  constexpr int kTile = kStepKeys * D;       // bytes of a staged tile
+  constexpr int kCols = D / 16;
+  constexpr int kSlots = row_slots(D);
+  constexpr int NR = R / 8;                  // rows of a lane
+  extern __shared__ __align__(128) uint8_t s_ring[];
   __shared__ long long s_sum[kRowWarps];
-  __shared__ long long s_first[2];
+  __shared__ long long s_upto[32 * kRowWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
+  const int worker = blockIdx.x * kRowWarps + warp;
+  const int bs = 1 << a.bs_log;
+  pdl_trigger();  // the join's blocks may take their places; they wait for this grid
 
-  // ---- this block's share of the steps of all items
+  // ---- this warp's share of the units of all items
   const int per_thread = (a.B + blockDim.x - 1) / blockDim.x;
-  const int b_lo = tid * per_thread, b_hi = min(a.B, b_lo + per_thread);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b)
-    mine += request_units(a, request_of(a, b, blockIdx.x == 0));
-  long long upto = mine;
+  {
+    const int b_lo = tid * per_thread, b_hi = min(a.B, b_lo + per_thread);
+    long long upto = 0;
+    for (int b = b_lo; b < b_hi; ++b)
+      upto += request_units<R>(a, request_of(a, b, blockIdx.x == 0));
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(kAll, upto, d);
-    if (lane >= d) upto += y;
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(kAll, upto, d);
+      if (lane >= d) upto += y;
+    }
+    if (lane == 31) s_sum[warp] = upto;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) upto += s_sum[i];
+    s_upto[tid] = upto;
+    __syncthreads();
   }
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  long long total = 0;
-  for (int i = 0; i < kRowWarps; ++i) {
-    if (i < warp) upto += s_sum[i];
-    total += s_sum[i];
-  }
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < a.min_steps) per = a.min_steps;
-  long long u = per * blockIdx.x;
+  const long long total = s_upto[32 * kRowWarps - 1];
+  const long long workers = (long long)gridDim.x * kRowWarps;
+  long long per = (total + workers - 1) / workers;
+  if (per < a.min_units) per = a.min_units;
+  long long u = per * worker;
   const long long u_end = min(total, u + per);
+  PartHead head = {0, 0, 0, -1};
   if (u >= u_end) {
-    if (tid == 0) a.heads[blockIdx.x].last = -1;
+    if (lane == 0) a.heads[worker] = head;
     return;
   }
-  if (upto - mine <= u && u < upto) {  // exactly one thread
-    long long before = upto - mine;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const long long x = request_units(a, request_of(a, b, false));
-      if (before + x > u) {
-        s_first[0] = b;
-        s_first[1] = before;
+  int b = 0;
+  long long b_units = 0;  // units before request b
+  {
+    int first = 0;  // threads whose requests end at or before u
+    for (int i = 0; i < kRowWarps; ++i)
+      first += __popc(__ballot_sync(kAll, s_upto[i * 32 + lane] <= u));
+    b = first * per_thread;
+    b_units = first ? s_upto[first - 1] : 0;
+    // 32 requests at a time
+    for (;;) {
+      const int mine = b + lane;
+      long long x = mine < a.B ? request_units<R>(a, request_of(a, mine, false)) : 0, upto = x;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(kAll, upto, d);
+        if (lane >= d) upto += y;
+      }
+      const int past = __popc(__ballot_sync(kAll, b_units + upto <= u));
+      if (past < 32) {
+        if (past) b_units += __shfl_sync(kAll, upto, past - 1);
+        b += past;
         break;
       }
-      before += x;
+      b_units += __shfl_sync(kAll, upto, 31);
+      b += 32;
     }
   }
-  __syncthreads();
-  int b = (int)s_first[0];
-  long long b_units = s_first[1];  // units before request b
-  PartHead head = {0, 0, 0, -1};
+  const uint32_t ring =
+      (uint32_t)__cvta_generic_to_shared(s_ring) + warp * (kSlots * 2 * kTile);
 
   while (u < u_end) {
     const Request req = request_of(a, b, false);
-    const int64_t tiles = row_tiles(a, req), steps = item_steps(a, req);
-    const long long x = tiles * a.H * steps;
-    if (b_units + x <= u) {
-      b_units += x;
+    const int64_t tiles = row_tiles<R>(a, req), units = item_units(a, req);
+    const long long all = tiles * a.H * units;
+    if (b_units + all <= u) {
+      b_units += all;
       ++b;
       continue;
     }
-    const int64_t item = (u - b_units) / steps;
-    const int64_t s0 = (u - b_units) % steps;
-    const int64_t s1 = min((long long)steps, s0 + (u_end - u));
+    const int64_t item = (u - b_units) / units;
+    const int64_t u0 = (u - b_units) % units;
+    const int64_t u1 = min((long long)units, u0 + (u_end - u));
     const int h = (int)(item / tiles);
     const int64_t tile = item % tiles;
     const int64_t rows = req.w * a.G;
+    const int64_t first_row = tile * R;
+    const int n_rows = (int)min((int64_t)R, rows - first_row);
+
+    // ---- keys that any row of the tile sees, and keys that all of them see; the
+    // steps of this share among the former
+    const int64_t t_lo = first_row / a.G, t_hi = (first_row + n_rows - 1) / a.G;
+    const int64_t p_lo = req.L - req.w + t_lo, p_hi = req.L - req.w + t_hi;
+    const int any_hi = (int)max((int64_t)0, a.causal ? min(req.L, p_hi + 1) : req.L);
+    const int any_lo = (int)max((int64_t)0, a.window ? p_lo - a.window + 1 : 0);
+    const int all_hi = (int)max((int64_t)0, a.causal ? min(req.L, p_lo + 1) : req.L);
+    const int all_lo = (int)max((int64_t)0, a.window ? p_hi - a.window + 1 : 0);
+    const int key0 = (int)first_key(a, req);
+    const int k_lo = max(key0 + (int)u0 * kUnitKeys, any_lo & ~15);
+    const int k_hi = (int)min((int64_t)any_hi, key0 + u1 * kUnitKeys);
+    const int n_steps = k_hi > k_lo ? (k_hi - k_lo + kStepKeys - 1) / kStepKeys : 0;
+
+    // Block id and scales of step 32 g + lane: group `c` of the steps that are
+    // computed and the next one, `n`.
+    int32_t id_c, id_n;
+    float ks_c, vs_c, ks_n, vs_n;
+    const int32_t* row_table = a.table + (int64_t)b * a.max_blocks;
+    auto look_up = [&](int s, int32_t& id, float& ks, float& vs) {
+      id = -1;
+      ks = vs = 0.f;
+      if (s < n_steps) {
+        id = __ldg(row_table + ((k_lo + s * kStepKeys) >> a.bs_log));
+        if (id < 0 || id >= a.num_blocks) {
+          id = -1;
+          set_status(a.status, kStBadBlock);
+        } else {
+          ks = __ldg(a.ks + (int64_t)id * a.H + h);
+          vs = __ldg(a.vs + (int64_t)id * a.H + h);
+        }
+      }
+    };
+    // this lane's chunks of head h: chunk i * 32 + lane of a tile
+    const int8_t* kb = a.k + ((int64_t)h << a.bs_log) * D + lane * 16;
+    const int8_t* vb = a.v + ((int64_t)h << a.bs_log) * D + lane * 16;
+    const int block_bytes = (a.H << a.bs_log) * D;
+    auto fetch = [&](int s, int32_t id, uint32_t to) {  // id: of step s, -1 for none
+      if (id >= 0) {
+        const int64_t off =
+            (int64_t)id * block_bytes + ((k_lo + s * kStepKeys) & (bs - 1)) * D;
+#pragma unroll
+        for (int i = 0; i < kTile / 512; ++i) {
+          const int row = i * (32 / kCols) + lane / kCols, col = lane % kCols;
+          copy16(to + staged<D, false>(row, col), kb + off + i * 512);
+          copy16(to + kTile + staged<D, true>(row, col), vb + off + i * 512);
+        }
+      }
+      copies_commit();
+    };
+    look_up(lane, id_c, ks_c, vs_c);
+#pragma unroll
+    for (int s = 0; s < kSlots - 1; ++s)
+      fetch(s, __shfl_sync(kAll, id_c, s), ring + s * (2 * kTile));
+    look_up(32 + lane, id_n, ks_n, vs_n);
+    uint32_t slot = ring, free_slot = ring + (kSlots - 1) * (2 * kTile);
 
     // ---- the tile's query rows
-    float inv[2];          // score factor of the lane's rows
-    int64_t row_hi[2], row_lo[2];
-    uint32_t qf[NQ][kK][4];
-    const int64_t first_row = tile * kRowTile;
-    const int n_rows = (int)min((int64_t)kRowTile, rows - first_row);
+    // B operands: lane (r, c) holds row 8 i + r.  Factors, limits, maxima and sums
+    // are kept where the results are: rows 8 i + 2c + k, index [i][k].
+    float inv[NR][2];
+    int row_hi[NR][2], row_lo[NR][2];
+    uint32_t qf[NQ][NR][kK][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t row = first_row + r + 8 * half;
+    for (int i = 0; i < NR; ++i) {
+      const int64_t row = first_row + r + 8 * i;
       const bool real = row < rows;
       const int64_t t = real ? row / a.G : 0;
       const T* p = static_cast<const T*>(a.q) + (req.start + t) * a.qsn +
@@ -280,309 +409,350 @@ __global__ void __launch_bounds__(32 * kRowWarps, NQ == 1 && D <= 64 ? 3 : 2) k_
           x[kk][0] = x[kk][1] = x[kk][2] = x[kk][3] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(x[kk][i]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 4; ++e) amax = max(amax, __float_as_uint(x[kk][e]) & 0x7FFFFFFFu);
       }
       amax = max(amax, __shfl_xor_sync(kAll, amax, 1));
       amax = max(amax, __shfl_xor_sync(kAll, amax, 2));
-      const float f = row_factor(amax);
-      inv[half] = __fdiv_rn(a.scale_log2, f);
+      // a negative softmax scale goes into the sign of the query
+      const float f = copysignf(row_factor(amax), a.scale_log2);
 #pragma unroll
       for (int kk = 0; kk < kK; ++kk) {
         float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = f != f ? 0.f : __fmul_rn(x[kk][i], f);
-        qf[0][kk][half] = half2_bits(y[0], y[1]);
-        qf[0][kk][half + 2] = half2_bits(y[2], y[3]);
+        for (int e = 0; e < 4; ++e) y[e] = f != f ? 0.f : __fmul_rn(x[kk][e], f);
+        qf[0][i][kk][0] = half2_bits(y[0], y[1]);
+        qf[0][i][kk][1] = half2_bits(y[2], y[3]);
         if constexpr (NQ == 2) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = __fsub_rn(y[i], __half2float(__float2half_rn(y[i])));
-          qf[NQ - 1][kk][half] = half2_bits(y[0], y[1]);
-          qf[NQ - 1][kk][half + 2] = half2_bits(y[2], y[3]);
+          for (int e = 0; e < 4; ++e) y[e] = __fsub_rn(y[e], __half2float(__float2half_rn(y[e])));
+          qf[NQ - 1][i][kk][0] = half2_bits(y[0], y[1]);
+          qf[NQ - 1][i][kk][1] = half2_bits(y[2], y[3]);
         }
       }
       const int64_t pos = req.L - req.w + t;
-      row_hi[half] = real ? (a.causal ? min(req.L, pos + 1) : req.L) : 0;
-      row_lo[half] = a.window ? pos - a.window + 1 : 0;
+      const float own = __fdiv_rn(a.scale_log2, f);
+      const int hi = real ? (int)max((int64_t)0, a.causal ? min(req.L, pos + 1) : req.L) : 0;
+      const int lo = a.window ? (int)max((int64_t)0, pos - a.window + 1) : 0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        inv[i][k] = __shfl_sync(kAll, own, 8 * c + 4 * k);
+        row_hi[i][k] = __shfl_sync(kAll, hi, 8 * c + 4 * k);
+        row_lo[i][k] = __shfl_sync(kAll, lo, 8 * c + 4 * k);
+      }
     }
-    // keys that any row of the tile sees, and keys that all of them see
-    const int64_t t_lo = first_row / a.G, t_hi = (first_row + n_rows - 1) / a.G;
-    const int64_t p_lo = req.L - req.w + t_lo, p_hi = req.L - req.w + t_hi;
-    const int64_t any_hi = a.causal ? min(req.L, p_hi + 1) : req.L;
-    const int64_t any_lo = a.window ? p_lo - a.window + 1 : 0;
-    const int64_t all_hi = a.causal ? min(req.L, p_lo + 1) : req.L;
-    const int64_t all_lo = a.window ? p_hi - a.window + 1 : 0;
-    const int64_t key0 = first_key(a, req) + warp * 16;
 
-    RowState<D> st;
+    // acc[i][t]: rows 8 i + 2c, 8 i + 2c + 1 of the lane's dims 2t, then of 2t + 1
+    float acc[NR][D / 16][4];
+    float m[NR][2], l[NR][2];  // running maxima (log2 units), sums over this lane's keys
+    float vref = 0.f;          // power of two above the value scales seen
+    float weight = 0.f;        // kWeightScale / vref
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) st.acc[i][0] = st.acc[i][1] = st.acc[i][2] = st.acc[i][3] = 0.f;
-    st.m[0] = st.m[1] = -CUDART_INF_F;
-    st.l[0] = st.l[1] = 0.f;
-    st.vref = 0.f;
+    for (int i = 0; i < NR; ++i) {
+      m[i][0] = m[i][1] = -CUDART_INF_F;
+      l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
+    }
 
-    // Block id and scales of step s0 + 32 g + lane, loaded one group ahead.
-    int32_t id_n = -1, id_l = -1;
-    float ks_n = 0.f, vs_n = 0.f, ks_l = 0.f, vs_l = 0.f;
-    auto look_up = [&](int64_t s) {
-      const int64_t key = key0 + s * kStepKeys;
-      id_n = -1;
-      if (s < s1 && key < any_hi && key + 16 > any_lo) {
-        id_n = a.table[(int64_t)b * a.max_blocks + (key >> a.bs_log)];
-        if (id_n < 0 || id_n >= a.num_blocks) {
-          id_n = -1;
-          set_status(a.status, kStBadBlock);
+    for (int s = 0; s < n_steps; ++s) {
+      const int at = s & 31;
+      if (at == 0 && s) {
+        id_c = id_n;
+        ks_c = ks_n;
+        vs_c = vs_n;
+        look_up(s + 32 + lane, id_n, ks_n, vs_n);
+      }
+      copies_wait<kSlots - 2>();
+      __syncwarp();  // every lane's copies of step s have landed, step s - 1 is read
+      fetch(s + kSlots - 1,
+            __shfl_sync(kAll, at + kSlots - 1 < 32 ? id_c : id_n, (s + kSlots - 1) & 31), free_slot);
+      const uint32_t kt = slot, vt = slot + kTile;
+      free_slot = slot;
+      slot = slot + 2 * kTile == ring + kSlots * 2 * kTile ? ring : slot + 2 * kTile;
+      const int32_t id = __shfl_sync(kAll, id_c, at);
+      float ks = __shfl_sync(kAll, ks_c, at);
+      const float vs = __shfl_sync(kAll, vs_c, at);
+      if (id < 0) continue;  // a block outside the cache
+      const int key = k_lo + s * kStepKeys;
+
+      uint32_t kw[2][kK];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = j * 8 + r;
+        if constexpr (D >= 64) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i)
+            lds_words<4>(kt + staged<D, false>(row, i * 4 + c), &kw[j][i * 4]);
         } else {
-          ks_n = a.ks[(int64_t)id_n * a.H + h];
-          vs_n = a.vs[(int64_t)id_n * a.H + h];
+          lds_words<2>(kt + row * D + c * 8, kw[j]);
         }
       }
-    };
-    uint32_t kw[2][2][kK], vw[2][4][kWV];  // [buffer]: key words, value words
-    int32_t id_of[2];
-    float ks_of[2], vs_of[2];
-    auto fetch = [&](int64_t s, int buf) {
-      const int at = (int)(s - s0) & 31;
-      if (at == 0) {
-        id_l = id_n;
-        ks_l = ks_n;
-        vs_l = vs_n;
-        look_up(s + 32 + lane);
+      uint32_t vw[4][kWV];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = 2 * c + (j & 1) + (j >> 1) * 8;
+        const int byte = r * (D / 8);  // of the row
+        lds_words<kWV>(vt + staged<D, true>(row, byte >> 4) + (byte & 15), vw[j]);
       }
-      const int32_t id = s < s1 ? __shfl_sync(kAll, id_l, at) : -1;
-      id_of[buf] = id;
-      ks_of[buf] = __shfl_sync(kAll, ks_l, at);
-      vs_of[buf] = __shfl_sync(kAll, vs_l, at);
-      if (id < 0) return;
-      const int64_t key = key0 + s * kStepKeys;
-      const int64_t off = ((((int64_t)id * a.H + h) << a.bs_log) + (key & ((1 << a.bs_log) - 1))) * D;
-      const int8_t* kp = a.k + off + r * D + c * (4 * kWK);
+      float sc[NR][4];  // [rows 8 i ..][2 j + k]: key r + 8 j, row 2c + k
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < NR; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-          load_words<kWK>(kp + j * 8 * D + i * 64, &kw[buf][j][i * kWK]);
-      const int8_t* vp = a.v + off + 2 * c * D + r * (D / 8);
+      for (int kk = 0; kk < kK; ++kk) {
+        const uint32_t x0 = kw[0][kk] ^ 0x80808080u, x1 = kw[1][kk] ^ 0x80808080u;
+        const uint32_t ka[4] = {codes_half2(x0, kSelLow), codes_half2(x1, kSelLow),
+                                codes_half2(x0, kSelHigh), codes_half2(x1, kSelHigh)};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        load_words<kWV>(vp + ((j & 1) + (j >> 1) * 8) * D, vw[buf][j]);
-    };
-    auto compute = [&](int64_t s, int buf) {
-      if (id_of[buf] < 0) return;
-      const int64_t key = key0 + s * kStepKeys;
-      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int kk = 0; kk < kK; ++kk)
+          for (int t = 0; t < NQ; ++t) mma_16816(sc[i], ka, qf[t][i][kk][0], qf[t][i][kk][1]);
+      }
+      const bool hide = key + kStepKeys > all_hi || key < all_lo;
+      uint32_t hidden = 0;  // bit i * 4 + 2 j + k
+      if (hide) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t x = kw[buf][j][kk] ^ 0x80808080u;
-          const uint32_t b0 = codes_half2(x, kSelLow), b1 = codes_half2(x, kSelHigh);
-          mma_16816(sc[j], qf[0][kk], b0, b1);
-          if constexpr (NQ == 2) mma_16816(sc[j], qf[NQ - 1][kk], b0, b1);
-        }
-      const float ks = isfinite(ks_of[buf]) ? ks_of[buf] : CUDART_NAN_F;
-      const float vs = vs_of[buf];
-      const float f[2] = {__fmul_rn(inv[0], ks), __fmul_rn(inv[1], ks)};
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[j][i] = __fmul_rn(sc[j][i], f[i >> 1]);
-      if (key + 16 > all_hi || key < all_lo) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int64_t at = key + j * 8 + 2 * c + (i & 1);
-            if (at >= row_hi[i >> 1] || at < row_lo[i >> 1]) sc[j][i] = -CUDART_INF_F;
+          for (int e = 0; e < 4; ++e) {
+            const int k = key + r + 8 * (e >> 1);
+            if (k >= row_hi[i][e & 1] || k < row_lo[i][e & 1]) {
+              sc[i][e] = -CUDART_INF_F;
+              hidden |= 1u << (i * 4 + e);
+            }
           }
       }
-      const float mx0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      const float mx1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+      if (ks < 0.f) {  // no append gives one
+        ks = -ks;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!(hidden >> (i * 4 + e) & 1)) sc[i][e] = -sc[i][e];
+      }
+      float f[NR][2], mx[NR][2];
+      bool up = false;
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          f[i][k] = __fmul_rn(inv[i][k], ks);
+          mx[i][k] = fmaxf(sc[i][k], sc[i][k + 2]);
+          mx[i][k] = mx[i][k] == -CUDART_INF_F ? mx[i][k] : __fmul_rn(mx[i][k], f[i][k]);
+          up |= mx[i][k] > m[i][k] + kSlack;
+        }
       const float va = fabsf(vs);
-      const bool vup = va > st.vref && va < CUDART_INF_F;
-      if (__any_sync(kAll, mx0 > st.m[0] + kSlack || mx1 > st.m[1] + kSlack || vup)) {
+      const bool vup = va > vref && va < CUDART_INF_F;
+      if (__any_sync(kAll, up || vup)) {
         float beta = 1.f;
-        if (vup) {  // the next power of two
+        if (vup) {  // the next power of two, twice the largest scale at most
           const uint32_t e = (__float_as_uint(va) >> 23) + 1;
           const float to = __uint_as_float((e > 254 ? 254 : e) << 23);
-          beta = __fdiv_rn(st.vref, to);
-          st.vref = to;
+          beta = __fdiv_rn(vref, to);
+          vref = to;
+          weight = __fdiv_rn(kWeightScale, vref);
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float mx = half ? mx1 : mx0;
-          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, 2));
-          const float to = fmaxf(st.m[half], mx);
-          const float alpha = to == st.m[half] ? 1.f : exp2_fast(st.m[half] - to);
-          st.m[half] = to;
-          st.l[half] = __fmul_rn(st.l[half], alpha);
-          const float g = __fmul_rn(alpha, beta);
+        for (int i = 0; i < NR; ++i) {
+          float g[2];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            st.acc[i][2 * half] = __fmul_rn(st.acc[i][2 * half], g);
-            st.acc[i][2 * half + 1] = __fmul_rn(st.acc[i][2 * half + 1], g);
+          for (int k = 0; k < 2; ++k) {
+            float x = mx[i][k];
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
+            const float to = fmaxf(m[i][k], x);
+            const float alpha = to == m[i][k] ? 1.f : exp2_fast(m[i][k] - to);
+            m[i][k] = to;
+            l[i][k] = __fmul_rn(l[i][k], alpha);
+            g[k] = __fmul_rn(alpha, beta);
           }
+#pragma unroll
+          for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][t][e] = __fmul_rn(acc[i][t][e], g[e & 1]);
         }
       }
-      const float pv = isfinite(vs) ? (st.vref > 0.f ? __fmul_rn(__fdiv_rn(vs, st.vref), kWeightScale) : 0.f)
-                                    : CUDART_NAN_F;
-      float p[2][4];
+      const float pv = __fmul_rn(weight, vs);
+      uint32_t pb[NP][NR][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < NR; ++i) {
+        float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float m = st.m[i >> 1];
-          const float e = exp2_fast(__fsub_rn(sc[j][i], m == -CUDART_INF_F ? 0.f : m));
-          st.l[i >> 1] = __fadd_rn(st.l[i >> 1], e);
-          // a hidden key has weight 0 whatever its block's scale is
-          p[j][i] = sc[j][i] == -CUDART_INF_F ? 0.f : __fmul_rn(e, pv);
+        for (int e = 0; e < 4; ++e) {
+          const float base = m[i][e & 1] == -CUDART_INF_F ? 0.f : m[i][e & 1];
+          // rounded like the maximum, so that the largest score gives 2^0 at any size
+          p[e] = exp2_fast(__fsub_rn(__fmul_rn(sc[i][e], f[i][e & 1]), base));
+          if (hide && (hidden >> (i * 4 + e) & 1)) p[e] = 0.f;
         }
-      uint32_t pa[NP][4];
+        l[i][0] = __fadd_rn(l[i][0], __fadd_rn(p[0], p[2]));
+        l[i][1] = __fadd_rn(l[i][1], __fadd_rn(p[1], p[3]));
 #pragma unroll
-      for (int t = 0; t < NP; ++t) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            pa[t][2 * j + half] = half2_bits(p[j][2 * half], p[j][2 * half + 1]);
-        if (t + 1 < NP) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              p[j][i] = __fsub_rn(p[j][i], __half2float(__float2half_rn(p[j][i])));
+        for (int e = 0; e < 4; ++e) {
+          p[e] = __fmul_rn(p[e], pv);
+          // weight 0 whatever the block's scale is
+          if (hide && (hidden >> (i * 4 + e) & 1)) p[e] = 0.f;
         }
+#pragma unroll
+        for (int t = 0; t < NP; ++t)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            pb[t][i][j] = transposed(half2_bits(p[2 * j], p[2 * j + 1]));
+            if (t + 1 < NP) {
+              p[2 * j] = __fsub_rn(p[2 * j], __half2float(__float2half_rn(p[2 * j])));
+              p[2 * j + 1] = __fsub_rn(p[2 * j + 1], __half2float(__float2half_rn(p[2 * j + 1])));
+            }
+          }
       }
 #pragma unroll
       for (int w = 0; w < kWV; ++w) {
         uint32_t x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = vw[buf][j][w] ^ 0x80808080u;
-        const uint32_t lo0 = __byte_perm(x[0], x[1], 0x5140), hi0 = __byte_perm(x[0], x[1], 0x7362);
-        const uint32_t lo1 = __byte_perm(x[2], x[3], 0x5140), hi1 = __byte_perm(x[2], x[3], 0x7362);
+        for (int j = 0; j < 4; ++j) x[j] = vw[j][w] ^ 0x80808080u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t sel = e & 1 ? kSelHigh : kSelLow;
-          const uint32_t b0 = codes_half2(e < 2 ? lo0 : hi0, sel);
-          const uint32_t b1 = codes_half2(e < 2 ? lo1 : hi1, sel);
-          mma_16816(st.acc[w * 4 + e], pa[0], b0, b1);
-          if constexpr (NP == 2) mma_16816(st.acc[w * 4 + e], pa[NP - 1], b0, b1);
+        for (int e = 0; e < 2; ++e) {  // dims 4w + 2e, 4w + 2e + 1 of the lane
+          const uint32_t sel = e ? 0x7362 : 0x5140;
+          const uint32_t near = __byte_perm(x[0], x[1], sel), far = __byte_perm(x[2], x[3], sel);
+          const uint32_t va4[4] = {codes_half2(near, kSelLow), codes_half2(near, kSelHigh),
+                                   codes_half2(far, kSelLow), codes_half2(far, kSelHigh)};
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int t = 0; t < NP; ++t)
+              mma_16816(acc[i][w * 2 + e], va4, pb[t][i][0], pb[t][i][1]);
         }
       }
-    };
-
-    look_up(s0 + lane);
-    fetch(s0, 0);
-    for (int64_t s = s0; s < s1; s += 2) {
-      fetch(s + 1, 1);
-      compute(s, 0);
-      fetch(s + 2, 0);
-      if (s + 1 < s1) compute(s + 1, 1);
     }
+    copies_wait<0>();
+    __syncwarp();  // the ring is free for the next item
 
-    // ---- the warps' parts of the item together
+    // ---- results: lane (r, c) holds dims r * D / 8 .. of rows 8 i + 2c + j
+    const bool begins = u0 == 0, ends = u1 == units;
+    const bool whole = begins && ends;
+    const float unit = __fmul_rn(vref, 1.f / kWeightScale);
+    float* part = a.parts + ((int64_t)worker * 2 + (begins ? 1 : 0)) * R * (D + 2);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      st.l[half] += __shfl_xor_sync(kAll, st.l[half], 1);
-      st.l[half] += __shfl_xor_sync(kAll, st.l[half], 2);
-      if (r + 8 * half < n_rows) {
-        float* to = &s_acc[warp][r + 8 * half][2 * c * (D / 8)];
+    for (int i = 0; i < NR; ++i) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < D / 8; i += 4)
-            *reinterpret_cast<float4*>(to + j * (D / 8) + i) =
-                make_float4(st.acc[i][2 * half + j], st.acc[i + 1][2 * half + j],
-                            st.acc[i + 2][2 * half + j], st.acc[i + 3][2 * half + j]);
-      }
-      if (c == 0) {
-        s_m[warp][r + 8 * half] = st.m[half];
-        s_l[warp][r + 8 * half] = st.l[half];
-      }
-    }
-    if (lane == 0) s_v[warp] = __fmul_rn(st.vref, 1.f / kWeightScale);
-    __syncthreads();
-    const bool begins = s0 == 0, ends = s1 == steps;
-    float* part = a.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRowTile * (D + 2);
-    for (int i = tid; i < n_rows * (D / 4); i += blockDim.x) {
-      const int row = i / (D / 4), d = i % (D / 4) * 4;
-      float M = s_m[0][row], L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int w = 1; w < kRowWarps; ++w) M = fmaxf(M, s_m[w][row]);
-#pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
-        const float l = s_l[w][row], m = s_m[w][row];
-        if (l == 0.f) continue;  // this warp saw no key of the row
-        const float e = m == -CUDART_INF_F ? 1.f : exp2_fast(m - M);
-        const float g = __fmul_rn(e, s_v[w]);
-        L = __fmaf_rn(l, e, L);
-        const float4 v = *reinterpret_cast<const float4*>(&s_acc[w][row][d]);
-        o[0] = __fmaf_rn(v.x, g, o[0]);
-        o[1] = __fmaf_rn(v.y, g, o[1]);
-        o[2] = __fmaf_rn(v.z, g, o[2]);
-        o[3] = __fmaf_rn(v.w, g, o[3]);
-      }
-      if (begins && ends) {
+      for (int j = 0; j < 2; ++j) {
+        const int row = 8 * i + 2 * c + j;
+        const float top = m[i][j];
+        float L = l[i][j];
+        L += __shfl_xor_sync(kAll, L, 4);
+        L += __shfl_xor_sync(kAll, L, 8);
+        L += __shfl_xor_sync(kAll, L, 16);
+        if (row >= n_rows) continue;
+        // a row that saw no key has an all-zero accumulator
+        const float g = whole ? (L == 0.f ? 0.f : __fdiv_rn(unit, L)) : unit;
         const int64_t at = first_row + row, t = at / a.G;
         const int hq = h * a.G + (int)(at % a.G);
-        const float g = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+        float o[D / 8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = L == 0.f ? 0.f : __fmul_rn(o[j], g);
-        store4<T>(static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh + d, o);
-        if (a.lse && d == 0)
-          a.lse[(req.start + t) * a.Hq + hq] =
-              L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
-      } else {
-        *reinterpret_cast<float2*>(part + row * (D + 2) + d) = make_float2(o[0], o[1]);
-        *reinterpret_cast<float2*>(part + row * (D + 2) + d + 2) = make_float2(o[2], o[3]);
-        if (d == 0) *reinterpret_cast<float2*>(part + row * (D + 2) + D) = make_float2(M, L);
+        for (int k = 0; k < D / 8; ++k) o[k] = __fmul_rn(acc[i][k / 2][2 * (k & 1) + j], g);
+        const int d = r * (D / 8);
+        if (whole) {
+          store_row<T>(static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh + d, o);
+          if (a.lse && r == 0)
+            a.lse[(req.start + t) * a.Hq + hq] =
+                L == 0.f ? -CUDART_INF_F : __fmul_rn(top + log2f(L), 0.6931471805599453f);
+        } else {
+          store_row<float>(part + row * D + d, o);
+          if (r == 0) *reinterpret_cast<float2*>(part + R * D + row * 2) = make_float2(top, L);
+        }
       }
     }
     if (begins && !ends) {
       head.b = b;
       head.h = h;
       head.tile = (int)tile;
-      head.last = (int)((b_units + (item + 1) * steps - 1) / per);
+      head.last = (int)((b_units + (item + 1) * units - 1) / per);
     }
-    u += s1 - s0;
-    __syncthreads();
+    u += u1 - u0;
   }
-  if (tid == 0) a.heads[blockIdx.x] = head;
+  if (lane == 0) a.heads[worker] = head;
 }
 
-// Joins the parts of the items that k_kv_rows split: block i takes the item that
-// begins in block i there and goes on into the next ones.
-template <int D, typename T>
-__global__ void __launch_bounds__(256) k_kv_join(AttendArgs a) {
+// Joins the parts of the items that k_kv_rows split.  Blocks (i, .) take the item
+// that begins in worker i's share there and goes on into the next ones.  With few
+// parts block (i, 0) gives every row a warp; with many, block (i, y) takes rows y,
+// y + gridDim.y, .. and its warps take every kJoinWarps-th part, the loads of a round
+// in flight together, and meet in shared memory.  All sums have a fixed order.
+constexpr int kJoinWarps = 8;
+template <int D, typename T, int R>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(AttendArgs a) {
   pdl_enter();
   const PartHead head = a.heads[blockIdx.x];
   if (head.last < 0) return;
+  const int first = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool few = head.last - first < 16;
+  if (few && blockIdx.y) return;
   const Request req = request_of(a, head.b, false);
-  const int64_t first_row = (int64_t)head.tile * kRowTile, rows = req.w * a.G;
-  const int n_rows = (int)min((int64_t)kRowTile, rows - first_row);
-  const int first = blockIdx.x;
-  constexpr int64_t kPart = (int64_t)kRowTile * (D + 2);
-  auto part = [&](int i) { return a.parts + ((int64_t)i * 2 + (i == first ? 1 : 0)) * kPart; };
-  for (int i = threadIdx.x; i < n_rows * (D / 4); i += blockDim.x) {
-    const int row = i / (D / 4), d = i % (D / 4) * 4;
-    float M = -CUDART_INF_F, L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = first; j <= head.last; ++j) M = fmaxf(M, part(j)[row * (D + 2) + D]);
-    for (int j = first; j <= head.last; ++j) {
-      const float* p = part(j) + row * (D + 2);
-      const float m = p[D], l = p[D + 1];
-      if (l == 0.f) continue;
-      const float e = m == -CUDART_INF_F ? 1.f : exp2_fast(m - M);
-      L = __fmaf_rn(l, e, L);
+  __shared__ float s_o[kJoinWarps][D];
+  constexpr int kPer = D / 32, kRound = 8;
+  constexpr int64_t kPart = (int64_t)R * (D + 2);
+  const float* own = a.parts + ((int64_t)first * 2 + 1) * kPart;
+  auto part = [&](int i) { return i == first ? own : a.parts + (int64_t)i * 2 * kPart; };
+  const int step = few ? 1 : kJoinWarps, rows_at_once = few ? kJoinWarps : gridDim.y;
+  for (int row = few ? warp : blockIdx.y; row < R; row += rows_at_once) {
+    const int64_t at = (int64_t)head.tile * R + row;
+    if (at >= req.w * a.G) return;
+    float M = -CUDART_INF_F;
+    for (int i = first + lane; i <= head.last; i += 32) M = fmaxf(M, part(i)[R * D + row * 2]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __fmaf_rn(p[d + k], e, o[k]);
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
+    // weight of a part; a part without a key has l = 0, one of NaN alone m = -inf
+    auto weight = [&](float m, float l) {
+      return l == 0.f ? 0.f : m == -CUDART_INF_F ? 1.f : exp2_fast(m - M);
+    };
+    float L = 0.f;
+    for (int i = first + lane; i <= head.last; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(part(i) + R * D + row * 2);
+      L = __fmaf_rn(ml.y, weight(ml.x, ml.y), L);
     }
-    const int64_t at = first_row + row, t = at / a.G;
-    const int hq = head.h * a.G + (int)(at % a.G);
-    const float g = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = L == 0.f ? 0.f : __fmul_rn(o[j], g);
-    store4<T>(static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh + d, o);
-    if (a.lse && d == 0)
+    for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
+    float o[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = 0.f;
+    for (int i0 = first + (few ? 0 : warp); i0 <= head.last; i0 += step * kRound) {
+      float x[kRound][kPer], e[kRound];
+#pragma unroll
+      for (int j = 0; j < kRound; ++j) {
+        const int i = i0 + j * step;
+        e[j] = 0.f;
+        if (i <= head.last) {
+          const float* p = part(i);
+          const float2 ml = *reinterpret_cast<const float2*>(p + R * D + row * 2);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) x[j][k] = p[row * D + lane + 32 * k];
+          e[j] = weight(ml.x, ml.y);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kRound; ++j)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (e[j] != 0.f) o[k] = __fmaf_rn(x[j][k], e[j], o[k]);
+    }
+    if (!few) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) s_o[warp][lane + 32 * k] = o[k];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+#pragma unroll
+          for (int w = 1; w < kJoinWarps; ++w) o[k] = __fadd_rn(o[k], s_o[w][lane + 32 * k]);
+      }
+      __syncthreads();  // s_o is free for the next row
+      if (warp) continue;
+    }
+    const int64_t t = at / a.G;
+    const int hq = head.h * a.G + (int)(at % a.G);
+    T* out = static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      out[lane + 32 * k] = (T)(L == 0.f ? 0.f : __fdiv_rn(o[k], L));
+    if (a.lse && lane == 0)
       a.lse[(req.start + t) * a.Hq + hq] =
           L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
   }

@@ -98,10 +98,10 @@ inline int allow_dynamic_smem(const void* kern, size_t bytes) {
 // stream drains (programmatic dependent launch: every kernel waits for its
 // predecessors with griddepcontrol.wait before touching memory).
 template <typename... KArgs, typename... Args>
-int launch(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t st, bool pdl,
+int launch(void (*kern)(KArgs...), dim3 grid, unsigned block, cudaStream_t st, bool pdl,
            Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = st;
@@ -120,12 +120,12 @@ int launch(void (*kern)(KArgs...), unsigned grid, unsigned block, cudaStream_t s
 }
 
 template <typename... KArgs, typename... Args>
-int launch_smem(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem,
+int launch_smem(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem,
                 cudaStream_t st, bool pdl, Args&&... args) {
   int rc = allow_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
   if (rc) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
