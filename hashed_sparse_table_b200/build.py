@@ -17,7 +17,8 @@ SOURCES = [os.path.join(CSRC, "mpzch.cu"), os.path.join(CSRC, "mpzch_res.cu"),
            os.path.join(CSRC, "mpzch_kv.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in
                   ("mpzch_kernels.cuh", "mpzch_tier.cuh", "mpzch_device.cuh", "mpzch_launch.cuh",
-                   "mpzch_internal.h", "mpzch_kv_kernels.cuh", "mpzch_kv_rows.cuh")] + [os.path.join(ROOT, "include", "mpzch.h")]
+                   "mpzch_internal.h", "mpzch_kv_kernels.cuh", "mpzch_kv_rows.cuh",
+                   "mpzch_kv_tiles.cuh")] + [os.path.join(ROOT, "include", "mpzch.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -11,6 +11,11 @@ __device__ __forceinline__ void set_status(int32_t* st, int bits) {
   if (st) atomicOr(st, bits);
 }
 
+// Waits on other warps or on copies in flight give up after this long and set
+// MPZCH_STATUS_TIMEOUT (far beyond any legitimate wait).
+constexpr int kStTimeout = 16;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s
+
 __device__ __forceinline__ uint64_t global_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

@@ -76,11 +76,6 @@ __device__ __forceinline__ void atomic_add_ll(long long* p, long long v) {
   atomicAdd(reinterpret_cast<unsigned long long*>(p), (unsigned long long)v);
 }
 
-// Waits on other warps or on copies in flight give up after this long and set
-// MPZCH_STATUS_TIMEOUT (far beyond any legitimate wait).
-constexpr int kStTimeout = 16;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s
-
 // Row of `k` by one thread scanning the whole window (first match in probe
 // order; the identity map holds at most one).  -1 if absent.  Loads of 8
 // slots are issued together.

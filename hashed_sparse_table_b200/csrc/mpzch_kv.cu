@@ -3,6 +3,7 @@
 #include "mpzch.h"
 #include "mpzch_internal.h"
 #include "mpzch_kv_rows.cuh"
+#include "mpzch_kv_tiles.cuh"
 #include "mpzch_launch.cuh"
 
 #include <cmath>
@@ -54,7 +55,19 @@ int64_t head_bytes() {
 }
 
 int64_t part_bytes(int dim) {
-  return head_bytes() + row_workers() * 2ll * kMaxRows * (dim + 2) * (int64_t)sizeof(float);
+  const int64_t rows = row_workers() * 2ll * kMaxRows, tiles = sm_count() * 2ll * kTileRows;
+  return head_bytes() + (rows > tiles ? rows : tiles) * (dim + 2) * (int64_t)sizeof(float);
+}
+
+template <int D, typename T>
+int launch_tiles(const AttendArgs& a, cudaStream_t st) {
+  constexpr int kBytes = TileSmem<D>::kBytes;
+  const unsigned grid = (unsigned)sm_count();
+  int rc = launch_smem(k_kv_tiles<D, T>, grid, kTileThreads, kBytes, st, true, a);
+  if (!rc)
+    rc = launch(k_kv_join<D, T, kTileRows>, dim3(grid, kTileRows / kJoinWarps), 32 * kJoinWarps, st,
+                true, a);
+  return rc;
 }
 
 template <int D, typename T, int R, int NQ, int NP>
@@ -76,6 +89,9 @@ int launch_rows(const AttendArgs& a, cudaStream_t st) {
 // Tiles of 8 rows where no request has more, else of 16.
 template <int D, typename T, int NQ, int NP>
 int launch_rows(const AttendArgs& a, cudaStream_t st) {
+  if constexpr (D >= 64 && sizeof(T) == 2) {
+    if ((int64_t)a.max_new * a.G > 16) return launch_tiles<D, T>(a, st);
+  }
   return (int64_t)a.max_new * a.G <= 8 ? launch_rows<D, T, 8, NQ, NP>(a, st)
                                        : launch_rows<D, T, 16, NQ, NP>(a, st);
 }

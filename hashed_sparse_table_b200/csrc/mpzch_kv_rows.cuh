@@ -671,9 +671,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
   if (lane == 0) a.heads[worker] = head;
 }
 
-// Joins the parts of the items that k_kv_rows split.  Blocks (i, .) take the item
-// that begins in worker i's share there and goes on into the next ones.  With few
-// parts block (i, 0) gives every row a warp; with many, block (i, y) takes rows y,
+// Joins the parts of the items that k_kv_rows or k_kv_tiles split.  Blocks (i, .) take
+// the item that begins in worker i's share there and goes on into the next ones.
+// With few parts every row gets a warp; with many, block (i, y) takes rows y,
 // y + gridDim.y, .. and its warps take every kJoinWarps-th part, the loads of a round
 // in flight together, and meet in shared memory.  All sums have a fixed order.
 constexpr int kJoinWarps = 8;
@@ -684,15 +684,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(AttendArgs a) {
   if (head.last < 0) return;
   const int first = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool few = head.last - first < 16;
-  if (few && blockIdx.y) return;
   const Request req = request_of(a, head.b, false);
   __shared__ float s_o[kJoinWarps][D];
   constexpr int kPer = D / 32, kRound = 8;
   constexpr int64_t kPart = (int64_t)R * (D + 2);
   const float* own = a.parts + ((int64_t)first * 2 + 1) * kPart;
   auto part = [&](int i) { return i == first ? own : a.parts + (int64_t)i * 2 * kPart; };
-  const int step = few ? 1 : kJoinWarps, rows_at_once = few ? kJoinWarps : gridDim.y;
-  for (int row = few ? warp : blockIdx.y; row < R; row += rows_at_once) {
+  const int step = few ? 1 : kJoinWarps, rows_at_once = few ? kJoinWarps * gridDim.y : gridDim.y;
+  for (int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; row < R; row += rows_at_once) {
     const int64_t at = (int64_t)head.tile * R + row;
     if (at >= req.w * a.G) return;
     float M = -CUDART_INF_F;
