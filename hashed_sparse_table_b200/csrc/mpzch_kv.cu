@@ -201,7 +201,7 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
                     int64_t workspace_bytes, int32_t* dev_status, void* stream) {
   const int bytes = type_bytes(dtype);
   const int64_t need = mpzch_kv_attend_workspace(q_heads, kv_heads, dim);
-  if (need < 0 || bytes == 0 || n < 0 || n > kMaxInt || !block_size_ok(block_size) ||
+  if (need < 0 || bytes == 0 || n < 0 || n > (kMaxInt - 1024) / q_heads || !block_size_ok(block_size) ||
       num_blocks < 0 || num_blocks > kMaxInt || max_blocks < 0 || n_requests < 0 ||
       n_requests > MPZCH_KV_MAX_REQUESTS || max_new < 0 || !std::isfinite(softmax_scale) ||
       window < 0 || (window > 0 && !causal) ||
@@ -241,7 +241,6 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
   a.osh = out_stride_h;
   a.lse = lse;
   a.status = dev_status;
-  a.most_rows = INT64_MAX;
   a.min_units = 1;
   a.max_new = max_new;
   a.heads = static_cast<PartHead*>(workspace);

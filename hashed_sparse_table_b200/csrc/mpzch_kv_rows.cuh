@@ -28,7 +28,6 @@ struct AttendArgs {
   int64_t osn, osh;
   float* lse;
   int32_t* status;
-  int64_t most_rows;  // requests with more rows are left to the tile kernel
   int min_units;      // units that a warp takes at least
   int max_new;        // the caller's bound on a request's rows: sizes the join's grid
   struct PartHead* heads;
@@ -41,19 +40,18 @@ struct PartHead {
   int32_t b, h, tile, last;
 };
 
+// n * Hq < 2^31 (checked by the host), so rows and positions are ints.
 struct Request {
-  int64_t start;  // first row of the batch
-  int64_t w;      // rows (new tokens)
-  int64_t L;      // keys
+  int start;  // first row of the batch
+  int w;      // rows (new tokens)
+  int L;      // keys
 };
 
 __device__ __forceinline__ Request request_of(const AttendArgs& a, int b, bool report) {
   Request r;
-  const int64_t s0 = a.cu[b], e0 = a.cu[b + 1], l0 = a.seq[b];
-  const int64_t most = (int64_t)a.max_blocks << a.bs_log;
-  const int64_t s = s0 < 0 ? 0 : s0 > a.n ? a.n : s0;
-  const int64_t e = e0 < s ? s : e0 > a.n ? a.n : e0;
-  const int64_t l = l0 < 0 ? 0 : l0 > most ? most : l0;
+  const int s0 = a.cu[b], e0 = a.cu[b + 1], l0 = a.seq[b];
+  const int n = (int)a.n, most = a.max_blocks << a.bs_log;
+  const int s = min(max(s0, 0), n), e = min(max(e0, s), n), l = min(max(l0, 0), most);
   if (report && (s != s0 || e != e0 || l != l0)) set_status(a.status, kStBadLen);
   r.start = s;
   r.w = e - s;
@@ -61,28 +59,35 @@ __device__ __forceinline__ Request request_of(const AttendArgs& a, int b, bool r
   return r;
 }
 
-// Keys [lo, hi) that the request's rows see between them, lo rounded down to 16.
-__device__ __forceinline__ int64_t first_key(const AttendArgs& a, const Request& r) {
-  if (!a.window) return 0;
-  const int64_t lo = r.L - r.w - a.window + 1;
-  return lo > 0 ? lo & ~(int64_t)15 : 0;
+// First key inside the window of position p.
+__device__ __forceinline__ int window_low(const AttendArgs& a, int p) {
+  return a.window && p >= a.window ? p - a.window + 1 : 0;
+}
+// One behind the last key that position p sees.
+__device__ __forceinline__ int causal_high(const AttendArgs& a, const Request& r, int p) {
+  return a.causal ? max(0, min(r.L, p + 1)) : r.L;
+}
+
+// First key that any row of the request sees, rounded down to 16.
+__device__ __forceinline__ int first_key(const AttendArgs& a, const Request& r) {
+  return window_low(a, r.L - r.w) & ~15;
 }
 
 // Units of one (head, row tile) of the request; every such item has the same
 // number, at least one.
-__device__ __forceinline__ int64_t item_units(const AttendArgs& a, const Request& r) {
-  const int64_t keys = r.L - first_key(a, r);
+__device__ __forceinline__ int item_units(const AttendArgs& a, const Request& r) {
+  const int keys = r.L - first_key(a, r);
   return keys > kUnitKeys ? (keys + kUnitKeys - 1) / kUnitKeys : 1;
 }
 
 template <int R>
-__device__ __forceinline__ int64_t row_tiles(const AttendArgs& a, const Request& r) {
-  return r.w * a.G > a.most_rows ? 0 : (r.w * a.G + R - 1) / R;
+__device__ __forceinline__ int row_tiles(const AttendArgs& a, const Request& r) {
+  return (r.w * a.G + R - 1) / R;
 }
 
 template <int R>
-__device__ __forceinline__ int64_t request_units(const AttendArgs& a, const Request& r) {
-  return row_tiles<R>(a, r) * a.H * item_units(a, r);
+__device__ __forceinline__ long long request_units(const AttendArgs& a, const Request& r) {
+  return (long long)(row_tiles<R>(a, r) * a.H) * item_units(a, r);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -313,33 +318,30 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
 
   while (u < u_end) {
     const Request req = request_of(a, b, false);
-    const int64_t tiles = row_tiles<R>(a, req), units = item_units(a, req);
-    const long long all = tiles * a.H * units;
+    const int tiles = row_tiles<R>(a, req), units = item_units(a, req);
+    const long long all = (long long)(tiles * a.H) * units;
     if (b_units + all <= u) {
       b_units += all;
       ++b;
       continue;
     }
-    const int64_t item = (u - b_units) / units;
-    const int64_t u0 = (u - b_units) % units;
-    const int64_t u1 = min((long long)units, u0 + (u_end - u));
-    const int h = (int)(item / tiles);
-    const int64_t tile = item % tiles;
-    const int64_t rows = req.w * a.G;
-    const int64_t first_row = tile * R;
-    const int n_rows = (int)min((int64_t)R, rows - first_row);
+    const long long into = u - b_units;
+    const int item = (into >> 32) ? (int)(into / units) : (int)((uint32_t)into / (uint32_t)units);
+    const int u0 = (int)(into - (long long)item * units);
+    const int u1 = (int)min((long long)units, u0 + (u_end - u));
+    const int h = item / tiles, tile = item % tiles;
+    const int rows = req.w * a.G, first_row = tile * R;
+    const int n_rows = min(R, rows - first_row);
 
     // ---- keys that any row of the tile sees, and keys that all of them see; the
     // steps of this share among the former
-    const int64_t t_lo = first_row / a.G, t_hi = (first_row + n_rows - 1) / a.G;
-    const int64_t p_lo = req.L - req.w + t_lo, p_hi = req.L - req.w + t_hi;
-    const int any_hi = (int)max((int64_t)0, a.causal ? min(req.L, p_hi + 1) : req.L);
-    const int any_lo = (int)max((int64_t)0, a.window ? p_lo - a.window + 1 : 0);
-    const int all_hi = (int)max((int64_t)0, a.causal ? min(req.L, p_lo + 1) : req.L);
-    const int all_lo = (int)max((int64_t)0, a.window ? p_hi - a.window + 1 : 0);
-    const int key0 = (int)first_key(a, req);
-    const int k_lo = max(key0 + (int)u0 * kUnitKeys, any_lo & ~15);
-    const int k_hi = (int)min((int64_t)any_hi, key0 + u1 * kUnitKeys);
+    const int p_lo = req.L - req.w + first_row / a.G;
+    const int p_hi = req.L - req.w + (first_row + n_rows - 1) / a.G;
+    const int any_hi = causal_high(a, req, p_hi), any_lo = window_low(a, p_lo);
+    const int all_hi = causal_high(a, req, p_lo), all_lo = window_low(a, p_hi);
+    const int key0 = first_key(a, req);
+    const int k_lo = max(key0 + u0 * kUnitKeys, any_lo & ~15);
+    const int k_hi = min(any_hi, key0 + u1 * kUnitKeys);
     const int n_steps = k_hi > k_lo ? (k_hi - k_lo + kStepKeys - 1) / kStepKeys : 0;
 
     // Block id and scales of step 32 g + lane: group `c` of the steps that are
@@ -393,11 +395,11 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
     uint32_t qf[NQ][NR][kK][2];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int64_t row = first_row + r + 8 * i;
+      const int row = first_row + r + 8 * i;
       const bool real = row < rows;
-      const int64_t t = real ? row / a.G : 0;
+      const int t = real ? row / a.G : 0;
       const T* p = static_cast<const T*>(a.q) + (req.start + t) * a.qsn +
-                   (h * a.G + (real ? row % a.G : 0)) * a.qsh;
+                   (h * a.G + (real ? row - t * a.G : 0)) * a.qsh;
       float x[kK][4];
       uint32_t amax = 0;
 #pragma unroll
@@ -429,10 +431,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
           qf[NQ - 1][i][kk][1] = half2_bits(y[2], y[3]);
         }
       }
-      const int64_t pos = req.L - req.w + t;
+      const int pos = req.L - req.w + t;
       const float own = __fdiv_rn(a.scale_log2, f);
-      const int hi = real ? (int)max((int64_t)0, a.causal ? min(req.L, pos + 1) : req.L) : 0;
-      const int lo = a.window ? (int)max((int64_t)0, pos - a.window + 1) : 0;
+      const int hi = real ? causal_high(a, req, pos) : 0;
+      const int lo = window_low(a, pos);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         inv[i][k] = __shfl_sync(kAll, own, 8 * c + 4 * k);
@@ -643,8 +645,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
         if (row >= n_rows) continue;
         // a row that saw no key has an all-zero accumulator
         const float g = whole ? (L == 0.f ? 0.f : __fdiv_rn(unit, L)) : unit;
-        const int64_t at = first_row + row, t = at / a.G;
-        const int hq = h * a.G + (int)(at % a.G);
+        const int at = first_row + row, t = at / a.G;
+        const int hq = h * a.G + at - t * a.G;
         float o[D / 8];
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) o[k] = __fmul_rn(acc[i][k / 2][2 * (k & 1) + j], g);
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
         if (whole) {
           store_row<T>(static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh + d, o);
           if (a.lse && r == 0)
-            a.lse[(req.start + t) * a.Hq + hq] =
+            a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
                 L == 0.f ? -CUDART_INF_F : __fmul_rn(top + log2f(L), 0.6931471805599453f);
         } else {
           store_row<float>(part + row * D + d, o);
@@ -663,8 +665,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
     if (begins && !ends) {
       head.b = b;
       head.h = h;
-      head.tile = (int)tile;
-      head.last = (int)((b_units + (item + 1) * units - 1) / per);
+      head.tile = tile;
+      head.last = (int)((b_units + (item + 1ll) * units - 1) / per);
     }
     u += u1 - u0;
   }
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(AttendArgs a) {
   auto part = [&](int i) { return i == first ? own : a.parts + (int64_t)i * 2 * kPart; };
   const int step = few ? 1 : kJoinWarps, rows_at_once = few ? kJoinWarps * gridDim.y : gridDim.y;
   for (int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; row < R; row += rows_at_once) {
-    const int64_t at = (int64_t)head.tile * R + row;
+    const int at = head.tile * R + row;
     if (at >= req.w * a.G) return;
     float M = -CUDART_INF_F;
     for (int i = first + lane; i <= head.last; i += 32) M = fmaxf(M, part(i)[R * D + row * 2]);
@@ -745,14 +747,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(AttendArgs a) {
       __syncthreads();  // s_o is free for the next row
       if (warp) continue;
     }
-    const int64_t t = at / a.G;
-    const int hq = head.h * a.G + (int)(at % a.G);
+    const int t = at / a.G;
+    const int hq = head.h * a.G + at - t * a.G;
     T* out = static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
       out[lane + 32 * k] = (T)(L == 0.f ? 0.f : __fdiv_rn(o[k], L));
     if (a.lse && lane == 0)
-      a.lse[(req.start + t) * a.Hq + hq] =
+      a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
           L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
   }
 }

@@ -9,12 +9,20 @@ constexpr int kTileRows = 256;   // two halves of 128, each with its softmax war
 constexpr int kTileKeys = 128;   // keys of one step
 constexpr int kGroups = kTileKeys / 16;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kTileThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kTileThreads = 512;  // four warpgroups; two warps of the last one idle
+// Registers a thread by warpgroup: 2 softmax, converters, the rest.  The launch gives
+// 512 x 128 = 65,536; the split takes 128 x (2 x 152 + 104 + 104) = 65,536.
+constexpr int kSoftRegs = 152, kConvRegs = 104, kRestRegs = 104;
+static_assert(128 * (2 * kSoftRegs + kConvRegs + kRestRegs) <= 65536);
 constexpr int kTileStages = 2;
 constexpr int kScaleSlots = 4;
+constexpr int kRawKeys = 64;     // keys of a raw slot: K low, K high, V low, V high of a step
+constexpr int kRawSlots = 4;
 
 // Shared memory: Q [2 halves][D / 64][128 rows][128 B], K and V stages
-// [D / 64][128 keys][128 B], all in the 128-byte swizzle, then the small fields.
+// [D / 64][128 keys][128 B], all in the 128-byte swizzle; then the codes as they come,
+// [slot][64 keys][D], and the small fields.
 template <int D>
 struct TileSmem {
   static constexpr int kPlane = 128 * 128;            // 64 dims of 128 rows
@@ -22,23 +30,10 @@ struct TileSmem {
   static constexpr int kQ = 0;
   static constexpr int kK = 2 * kOperand;
   static constexpr int kV = kK + kTileStages * kOperand;
-  static constexpr int kSmall = kV + kTileStages * kOperand;
-  static constexpr int kBytes = kSmall + 1024 + 1024;  // and up to 1 KB to align the base
+  static constexpr int kRaw = kV + kTileStages * kOperand;
+  static constexpr int kSmall = kRaw + kRawSlots * kRawKeys * D;
+  static constexpr int kBytes = kSmall + 2048 + 1024;  // and up to 1 KB to align the base
 };
-
-struct TileSmall {
-  uint64_t k_full[kTileStages], v_full[kTileStages], k_free[kTileStages], v_free[kTileStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scales[kScaleSlots];
-  float ks[kScaleSlots][kGroups], vs[kScaleSlots][kGroups];
-  uint32_t hidden[kScaleSlots];  // bit g: group g has no block
-  uint32_t tmem;
-  int32_t failed;
-  int32_t b;
-  int32_t pad;
-  long long units, before;
-  long long sums[16];
-};
-static_assert(sizeof(TileSmall) <= 1024);
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -60,9 +55,19 @@ __device__ __forceinline__ bool bar_test(uint64_t* b, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_t bytes, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+      "l"(from), "r"(bytes), "r"(smem_addr(b))
+      : "memory");
+}
 // Waits for a phase; gives up after kWaitLimitNs (then, and once any warp of the
 // block gave up, false).
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, TileSmall* sm,
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int32_t* failed,
                                          int32_t* status) {
   if (bar_test(b, parity)) return true;
   const uint64_t t0 = global_ns();
@@ -70,9 +75,9 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, TileSmall
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (bar_test(b, parity)) return true;
-    if (*reinterpret_cast<volatile int32_t*>(&sm->failed)) return false;
+    if (*failed) return false;
     if (global_ns() - t0 > kWaitLimitNs) {
-      *reinterpret_cast<volatile int32_t*>(&sm->failed) = 1;
+      *failed = 1;
       set_status(status, kStTimeout);
       return false;
     }
@@ -101,10 +106,11 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32
   return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lead >> 4) & 0x3FFF) << 16 |
          (uint64_t)((stride >> 4) & 0x3FFF) << 32 | 1ull << 46 | 2ull << 61;
 }
-// fp16 x fp16 -> fp32, M = 128, N columns; B's N index contiguous if kTransposed.
-template <int N, bool kTransposed>
+// fp16 x fp16 (bf16 x bf16) -> fp32, M = 128, N columns; B's N index contiguous if
+// kTransposed.
+template <int N, bool kTransposed, bool kBf16>
 __device__ __forceinline__ constexpr uint32_t instruction() {
-  return 1u << 4 | (kTransposed ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
+  return 1u << 4 | (kBf16 ? 1u << 7 | 1u << 10 : 0u) | (kTransposed ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -161,45 +167,87 @@ __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
+  return x;
+}
+// Bits of the keys k0 .. k0 + 31 that lie in [lo, hi).
+__device__ __forceinline__ uint32_t keys_between(int k0, int lo, int hi) {
+  const int from = max(0, lo - k0), to = min(32, hi - k0);
+  if (to <= from || from > 31) return 0;
+  return (to == 32 ? kAll : (1u << to) - 1) & ~((1u << from) - 1);
+}
+
 // Keys [lo, hi) that any row of the row tile sees, lo rounded down to 16, and the
 // tile's steps (at least one).
 struct TileRange {
   int lo, hi, steps;
 };
-__device__ __forceinline__ TileRange tile_range(const AttendArgs& a, const Request& r, int64_t tile) {
-  const int64_t row0 = tile * kTileRows, row1 = min(row0 + kTileRows, r.w * a.G) - 1;
-  const int64_t p0 = r.L - r.w + row0 / a.G, p1 = r.L - r.w + row1 / a.G;
-  const int64_t lo = a.window ? p0 - a.window + 1 : 0;
+__device__ __forceinline__ TileRange tile_range(const AttendArgs& a, const Request& r, int tile) {
+  const int row0 = tile * kTileRows, row1 = min(row0 + kTileRows, r.w * a.G) - 1;
+  const int p0 = r.L - r.w;
   TileRange t;
-  t.lo = (int)max((int64_t)0, lo) & ~15;
-  t.hi = (int)max((int64_t)0, a.causal ? min(r.L, p1 + 1) : r.L);
+  t.lo = a.window ? window_low(a, p0 + row0 / a.G) & ~15 : 0;
+  t.hi = a.causal ? causal_high(a, r, p0 + row1 / a.G) : r.L;
   t.steps = t.hi > t.lo ? (t.hi - t.lo + kTileKeys - 1) / kTileKeys : 1;
   return t;
 }
 
-// Walks the items (request, kv head, row tile) of a block's share of the steps, the
-// same way in every warp.
+// Beginning and ending an item (queries, result) costs a block about as much as this
+// many steps; shares count an item as kItemCost + steps.
+constexpr int kItemCost = 1;
+
+// Walks the items (request, kv head, row tile) of a block's share of the work, the
+// same way in every warp.  A share that holds only the first kItemCost units of an
+// item leaves it to the next one.
 struct TileWalk {
   long long u, u_end;
   Request req;
-  long long head_units;  // steps of one head of the request
-  int64_t tiles, tile;
+  long long head_units;  // cost of one head of the request
   TileRange range;
-  int b, h, s0, s1;      // steps [s0, s1) of the item are this block's
+  int tiles, tile, b, h, x0, x1;  // the share takes units [x0, x1) of the item,
+  int s0, s1;                     // which are its steps [s0, s1)
 
-  __device__ __forceinline__ static long long steps_of(const AttendArgs& a, const Request& r,
+  __device__ __forceinline__ static long long cost_of(const AttendArgs& a, const Request& r,
                                                        int from, int stride) {
     long long x = 0;
-    const int64_t n = (r.w * a.G + kTileRows - 1) / kTileRows;
-    for (int64_t t = from; t < n; t += stride) x += tile_range(a, r, t).steps;
+    const int n = (r.w * a.G + kTileRows - 1) / kTileRows;
+    if (!a.causal && !a.window)  // every tile sees every key
+      return from < n ? ((n - 1 - from) / stride + 1ll) * (kItemCost + tile_range(a, r, 0).steps) : 0;
+    for (int t = from; t < n; t += stride) x += kItemCost + tile_range(a, r, t).steps;
     return x;
   }
-  // Whole-warp: the request's steps of one head.
+  // Whole-warp: the cost of one head of the request.
   __device__ __forceinline__ void enter(const AttendArgs& a, int to) {
     b = to;
     req = request_of(a, b, false);
     tiles = (req.w * a.G + kTileRows - 1) / kTileRows;
-    long long x = steps_of(a, req, threadIdx.x & 31, 32);
+    long long x = cost_of(a, req, threadIdx.x & 31, 32);
 #pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
     head_units = x;
@@ -214,16 +262,26 @@ struct TileWalk {
     into -= h * head_units;
     tile = 0;
     range = tile_range(a, req, 0);
-    while (into >= range.steps) {
-      into -= range.steps;
+    while (into >= kItemCost + range.steps) {
+      into -= kItemCost + range.steps;
       range = tile_range(a, req, ++tile);
     }
-    s0 = (int)into;
-    s1 = (int)min((long long)range.steps, s0 + (u_end - u));
+    x0 = (int)into;
+    cut();
+    if (s0 == s1) next(a);
   }
-  __device__ __forceinline__ bool next(const AttendArgs& a) {  // false behind the last item
-    u += s1 - s0;
-    if (u >= u_end) return false;
+  __device__ __forceinline__ void cut() {
+    x1 = (int)min((long long)(kItemCost + range.steps), x0 + (u_end - u));
+    s0 = max(0, x0 - kItemCost);
+    s1 = max(0, x1 - kItemCost);
+  }
+  // To the next item with steps in the share; s0 == s1 and false where there is none.
+  __device__ __forceinline__ bool next(const AttendArgs& a) {
+    u += x1 - x0;
+    if (u >= u_end) {
+      s0 = s1 = 0;
+      return false;
+    }
     if (++tile == tiles) {
       tile = 0;
       if (++h == a.H) {
@@ -233,12 +291,50 @@ struct TileWalk {
       }
     }
     range = tile_range(a, req, tile);
-    s0 = 0;
-    s1 = (int)min((long long)range.steps, u_end - u);
-    return true;
+    x0 = 0;
+    cut();
+    return s1 > s0;  // a share that ends inside the cost of an item has nothing behind it
+  }
+  __device__ __forceinline__ bool begins() const { return s0 == 0; }
+  __device__ __forceinline__ bool ends() const { return s1 == range.steps; }
+  // Block whose share ends the item.
+  __device__ __forceinline__ int last_block(long long per) const {
+    return (int)((u - x0 + kItemCost + range.steps - 1) / per);
   }
 };
 
+struct TileSmall {
+  uint64_t full[2][kTileStages], free[2][kTileStages];  // [K, V]
+  uint64_t raw_full[kRawSlots], raw_free[kRawSlots];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scales[kScaleSlots];
+  float2 scale[kScaleSlots][kGroups];  // |key scale|, log2 |value scale| of a group
+  float top[kScaleSlots];              // largest finite |value scale| of the step
+  uint32_t hidden[kScaleSlots];  // bit g: group g has no block
+  uint32_t negative[kScaleSlots];  // bit g, 8 + g: its key, value scale is negative
+  TileWalk ahead[kSoftWarps];  // the softmax warps' next items
+  int32_t failed;
+  uint32_t tmem;
+  int32_t b;
+  int32_t pad;
+  long long units, before;
+  long long sums[kTileThreads / 32];
+};
+static_assert(sizeof(TileSmall) <= 2048);
+
+// 8 codes (two words) as 16 bytes of bf16, times sign (+-1): 0x4300 | low 7 bits is
+// 128 + low, 0x4300 | bit 7 is 128 or 256, and their difference is the code, exactly.
+__device__ __forceinline__ uint4 codes_to_bf8(uint2 w, bool minus) {
+  uint32_t h[4];
+  const uint32_t sign2 = minus ? 0xBF80BF80u : 0x3F803F80u, flip = minus ? 0u : 0x80008000u;
+  const uint32_t m[4] = {__byte_perm(w.x, 0x43434343u, kSelLow), __byte_perm(w.x, 0x43434343u, kSelHigh),
+                         __byte_perm(w.y, 0x43434343u, kSelLow), __byte_perm(w.y, 0x43434343u, kSelHigh)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(h[i])
+        : "r"(m[i] & 0xFF7FFF7Fu), "r"(sign2), "r"((m[i] & 0xFF80FF80u) ^ flip));
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
 // 8 codes (two words) as 16 bytes of fp16, times sign (+-1).
 __device__ __forceinline__ uint4 codes_to_half8(uint2 w, uint32_t sign2, uint32_t off2) {
   uint32_t h[4];
@@ -250,11 +346,16 @@ __device__ __forceinline__ uint4 codes_to_half8(uint2 w, uint32_t sign2, uint32_
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[i]) : "r"(m[i]), "r"(sign2), "r"(off2));
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
+__device__ __forceinline__ void sts16(uint32_t to, uint4 y) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+               : "memory");
+}
 constexpr uint32_t kPlus2 = 0x3C003C00u, kMinus2 = 0xBC00BC00u;      // 1, -1
 constexpr uint32_t kOffPlus2 = 0xE480E480u, kOffMinus2 = 0x64806480u;  // -1152, 1152
 
-// One block an SM.  Per step of 128 keys a converter warpgroup turns the codes of K
-// and V into fp16 operands in shared memory (two stages), one thread issues
+// One block an SM.  Per step of 128 keys a loader warp brings the codes of K and V into
+// shared memory (bulk copies of 16 tokens, four slots of 64), a converter warpgroup
+// turns them into fp16 operands there (two stages), one thread issues
 //   S_i = Q_i K^T (i = 0, 1: the two halves of 128 rows), O_i += P_i V
 // with S and O in TMEM, and a warpgroup for each half turns S_i into P_i: a thread is
 // a row.  P_i takes the place of S_i in TMEM as fp16 pairs.  The halves alternate
@@ -268,13 +369,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   pdl_enter();
   pdl_trigger();
   using L = TileSmem<D>;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);  // queries and keys go as they are
   extern __shared__ __align__(16) uint8_t s_tile[];
   const uint32_t base = (smem_addr(s_tile) + 1023) & ~1023u;
   TileSmall* sm = reinterpret_cast<TileSmall*>(s_tile + (base - smem_addr(s_tile)) + L::kSmall);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kTileThreads / 32;
 
-  if (warp == kSoftWarps + kConvWarps) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&sm->tmem))
                  : "memory");
@@ -282,10 +384,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   }
   if (tid == 0) {
     for (int i = 0; i < kTileStages; ++i) {
-      bar_init(&sm->k_full[i], 32 * kConvWarps);
-      bar_init(&sm->v_full[i], 32 * kConvWarps);
-      bar_init(&sm->k_free[i], 1);
-      bar_init(&sm->v_free[i], 1);
+      bar_init(&sm->full[0][i], 32 * kConvWarps);
+      bar_init(&sm->full[1][i], 32 * kConvWarps);
+      bar_init(&sm->free[0][i], 1);
+      bar_init(&sm->free[1][i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm->q_full[i], 128);
@@ -294,6 +396,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       bar_init(&sm->o_full[i], 1);
     }
     for (int i = 0; i < kScaleSlots; ++i) bar_init(&sm->scales[i], 1);
+    for (int i = 0; i < kRawSlots; ++i) {
+      bar_init(&sm->raw_full[i], 1);
+      bar_init(&sm->raw_free[i], 32 * kConvWarps);
+    }
     sm->failed = 0;
     sm->b = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -309,7 +415,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   long long mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const Request r = request_of(a, b, blockIdx.x == 0);
-    mine += TileWalk::steps_of(a, r, by_warp ? lane : 0, by_warp ? 32 : 1) * a.H;
+    mine += TileWalk::cost_of(a, r, by_warp ? lane : 0, by_warp ? 32 : 1) * a.H;
   }
   long long incl = mine;  // inclusive over lanes
 #pragma unroll
@@ -336,7 +442,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       long long at = from;
       for (int b = b_lo; b < b_hi; ++b) {
         const Request r = request_of(a, b, false);
-        long long x = TileWalk::steps_of(a, r, by_warp ? lane : 0, by_warp ? 32 : 1) * a.H;
+        long long x = TileWalk::cost_of(a, r, by_warp ? lane : 0, by_warp ? 32 : 1) * a.H;
         if (by_warp) {
 #pragma unroll
           for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
@@ -354,14 +460,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   }
   __syncthreads();
   const uint32_t tmem = sm->tmem;
-  const bool any = u0 < u_end;
+  bool any = u0 < u_end;
   TileWalk walk;
-  if (any) walk.start(a, sm->b, u0 - sm->before, u0, u_end);
+  if (any) {
+    walk.start(a, sm->b, u0 - sm->before, u0, u_end);
+    any = walk.s1 > walk.s0;
+  }
 
   if (!any) {
     // no steps here
   } else if (warp < kSoftWarps) {
     // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int half = warp >> 2;
     const int at_row = (warp & 3) * 32 + lane;  // of the half = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -369,110 +479,135 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
     uint32_t n_s = 0, n_o = 0, n_k = 0;  // s_full and o_full phases, steps so far
     PartHead head = {0, 0, 0, -1};
     bool ok = true;
+    // The row's queries go into shared memory as they are (products of 16-bit values
+    // with codes are exact), 16 bytes a copy.  The next item's are asked for when the
+    // last scores of this one are there, and so come under its last step.
+    const float inv = fabsf(a.scale_log2);
+    const uint32_t q_at = base + L::kQ + half * L::kOperand + at_row * 128;
+    auto fetch_q = [&](const TileWalk& w) {
+      const int row = w.tile * kTileRows + half * 128 + at_row;
+      const bool real = row < w.req.w * a.G;
+      const int t = real ? row / a.G : 0;
+      const T* q = static_cast<const T*>(a.q) + (w.req.start + t) * a.qsn +
+                   (w.h * a.G + (real ? row - t * a.G : 0)) * a.qsh;
+#pragma unroll
+      for (int d = 0; d < D; d += 8) {
+        const uint32_t to = q_at + (d / 64) * L::kPlane + (((d % 64) * 2) ^ ((at_row & 7) << 4));
+        if (real)
+          copy16(to, reinterpret_cast<const int8_t*>(q + d));
+        else
+          sts16(to, make_uint4(0, 0, 0, 0));
+      }
+      copies_commit();
+    };
+    auto has_rows = [&](const TileWalk& w) {
+      return w.tile * kTileRows + half * 128 < w.req.w * a.G;
+    };
+    auto publish_q = [&] {
+      copies_wait<0>();
+      proxy_fence();
+      bar_arrive(&sm->q_full[half]);
+    };
+    if (has_rows(walk)) {
+      fetch_q(walk);
+      publish_q();
+    }
+    // the next item waits in shared memory: its fields would cost the loop registers
+    TileWalk* ahead = &sm->ahead[warp];
+    if (lane == 0) *ahead = walk;
+    bool more = true;
     do {
+      __syncwarp();
+      walk = *ahead;
+      const int n_steps = walk.s1 - walk.s0, first_key = walk.range.lo + walk.s0 * kTileKeys;
+      const bool begins = walk.begins(), ends = walk.ends();
       const Request req = walk.req;
-      const int64_t rows = req.w * a.G, row0 = walk.tile * kTileRows + half * 128;
-      const int n_steps = walk.s1 - walk.s0;
-      const bool begins = walk.s0 == 0, ends = walk.s1 == walk.range.steps;
+      const int row0 = walk.tile * kTileRows + half * 128, h = walk.h;
       if (begins && !ends) {
         head.b = walk.b;
         head.h = walk.h;
-        head.tile = (int)walk.tile;
-        head.last = (int)((walk.u + walk.range.steps - 1) / per);
+        head.tile = walk.tile;
+        head.last = walk.last_block(per);
       }
+      more = walk.next(a);
+      const bool next_here = more && has_rows(walk);
+      __syncwarp();
+      if (lane == 0) *ahead = walk;
+      __syncwarp();
+      const int rows = req.w * a.G;
       if (row0 >= rows) {  // this half of the tile is empty
         n_k += n_steps;
+        if (next_here) {
+          fetch_q(*ahead);
+          publish_q();
+        }
         continue;
       }
-      const int64_t row = row0 + at_row;
+      const int row = row0 + at_row;
       const bool real = row < rows;
-      const int64_t t = real ? row / a.G : 0;
-      const int hq = walk.h * a.G + (int)(real ? row % a.G : 0);
-      // ---- the row's queries, scaled by a power of two, as fp16 in shared memory
-      const T* q = static_cast<const T*>(a.q) + (req.start + t) * a.qsn + hq * a.qsh;
-      uint32_t amax = 0;
-      if (real) {
-#pragma unroll
-        for (int d = 0; d < D; d += 8) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + d));
-          const T* x = reinterpret_cast<const T*>(&v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            amax = max(amax, __float_as_uint((float)x[e]) & 0x7FFFFFFFu);
-        }
-      }
-      const float qfac = copysignf(row_factor(amax), a.scale_log2);
-      const float inv = __fdiv_rn(a.scale_log2, qfac);
-      const uint32_t q_at = base + L::kQ + half * L::kOperand + at_row * 128;
-#pragma unroll
-      for (int d = 0; d < D; d += 8) {
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (real && qfac == qfac) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + d));
-          const T* x = reinterpret_cast<const T*>(&v);
-          y.x = half2_bits(__fmul_rn((float)x[0], qfac), __fmul_rn((float)x[1], qfac));
-          y.y = half2_bits(__fmul_rn((float)x[2], qfac), __fmul_rn((float)x[3], qfac));
-          y.z = half2_bits(__fmul_rn((float)x[4], qfac), __fmul_rn((float)x[5], qfac));
-          y.w = half2_bits(__fmul_rn((float)x[6], qfac), __fmul_rn((float)x[7], qfac));
-        }
-        const uint32_t to = q_at + (d / 64) * L::kPlane + (((d % 64) * 2) ^ ((at_row & 7) << 4));
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(y.x), "r"(y.y), "r"(y.z),
-                     "r"(y.w)
-                     : "memory");
-      }
-      proxy_fence();
-      bar_arrive(&sm->q_full[half]);
-
-      const int64_t pos = req.L - req.w + t;
-      const int hi = real ? (int)max((int64_t)0, a.causal ? min(req.L, pos + 1) : req.L) : 0;
-      const int lo = a.window ? (int)max((int64_t)0, pos - a.window + 1) : 0;
+      const int t = real ? row / a.G : 0;
+      const int hq = h * a.G + (real ? row - t * a.G : 0);
+      const int pos = req.L - req.w + t;
+      const int hi = real ? causal_high(a, req, pos) : 0;
+      const int lo = window_low(a, pos);
       float m = -CUDART_INF_F, sum = 0.f;
+      bool seen = false;             // a key of this share
       float vref = 0.f, lref = 0.f;  // power of two above the value scales, its log2
       for (int j = 0; j < n_steps && ok; ++j, ++n_k) {
-        const int key = walk.range.lo + (walk.s0 + j) * kTileKeys;
+        const int key = first_key + j * kTileKeys;
         const int slot = n_k % kScaleSlots;
-        ok = bar_wait(&sm->scales[slot], (n_k / kScaleSlots) & 1, sm, a.status) &&
-             bar_wait(&sm->s_full[half], n_s & 1, sm, a.status);
+        ok = bar_wait(&sm->scales[slot], (n_k / kScaleSlots) & 1, &sm->failed, a.status) &&
+             bar_wait(&sm->s_full[half], n_s & 1, &sm->failed, a.status);
         if (!__all_sync(kAll, ok)) {
           ok = false;
           break;
         }
         ++n_s;
         tc_fence_after();
-        const float* ks = sm->ks[slot];
-        const float* vs = sm->vs[slot];
+        const bool fetched = j == n_steps - 1 && next_here;
+        if (fetched) fetch_q(*ahead);
+        const float2* scale = sm->scale[slot];
+        const float va = sm->top[slot];
         const uint32_t none = sm->hidden[slot];
         // does every row of the warp see every key?  (real rows; the others' results
         // are not used)
         const bool hide =
             none || __any_sync(kAll, real && (key + kTileKeys > hi || key < lo));
-        // ---- largest score
-        float mx = -CUDART_INF_F, va = 0.f;
-        uint32_t x[2][32];
-        tmem_load32(t_s, x[0]);
+        // keys that this row sees: in [lo, hi) and of a block that is there
+        auto visible = [&](int cnk) {
+          const uint32_t gone = none >> (cnk * 2);
+          return keys_between(key + cnk * 32, lo, hi) & ((gone & 1 ? 0 : 0xFFFFu) |
+                                                        (gone & 2 ? 0 : 0xFFFF0000u));
+        };
+        // ---- largest score.  The loops over 32 keys stay loops: unrolled, the block's
+        // roles together overran the instruction cache.
+        float mx = -CUDART_INF_F;
+        auto largest = [&](int cnk, uint32_t (&y)[32]) {
+          if (hide) {
+            const uint32_t vis = visible(cnk);
 #pragma unroll
-        for (int cnk = 0; cnk < 4; ++cnk) {
-          uint32_t (&y)[32] = x[cnk & 1];
-          tmem_loaded(y);
-          if (cnk < 3) tmem_load32(t_s + (cnk + 1) * 32, x[(cnk + 1) & 1]);
+            for (int e = 0; e < 32; ++e) y[e] = vis >> e & 1 ? y[e] : 0xFF800000u;
+          }
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const float f = __fmul_rn(inv, fabsf(ks[cnk * 2 + g]));
-            const float v = fabsf(vs[cnk * 2 + g]);
-            if (v < CUDART_INF_F) va = fmaxf(va, v);
-            float best = -CUDART_INF_F;
-            if (hide) {
-              const int k0 = key + cnk * 32 + g * 16;
-              const int to = none >> (cnk * 2 + g) & 1 ? lo : hi;
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (k0 + e < to && k0 + e >= lo) best = fmaxf(best, __uint_as_float(y[g * 16 + e]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) best = fmaxf(best, __uint_as_float(y[g * 16 + e]));
-            }
+            const float f = __fmul_rn(inv, scale[cnk * 2 + g].x);
+            const float* z = reinterpret_cast<const float*>(y) + g * 16;
+            float best = max3(max3(z[0], z[1], z[2]), max3(z[3], z[4], z[5]), max3(z[6], z[7], z[8]));
+            best = max3(best, max3(z[9], z[10], z[11]), max3(z[12], z[13], z[14]));
+            best = fmaxf(best, z[15]);
             if (best > -CUDART_INF_F) mx = fmaxf(mx, __fmul_rn(best, f));
           }
+        };
+        uint32_t y0[32], y1[32];
+        tmem_load32(t_s, y0);
+#pragma unroll 1
+        for (int cnk = 0; cnk < 4; cnk += 2) {
+          tmem_loaded(y0);
+          tmem_load32(t_s + (cnk + 1) * 32, y1);
+          largest(cnk, y0);
+          tmem_loaded(y1);
+          if (cnk == 0) tmem_load32(t_s + 64, y0);
+          largest(cnk + 1, y1);
         }
         const bool vup = va > vref;
         if (__any_sync(kAll, mx > m + kSlack) || vup) {
@@ -490,14 +625,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           sum = __fmul_rn(sum, alpha);
           if (j > 0) {
             const float g = __fmul_rn(alpha, beta);
-#pragma unroll
+#pragma unroll 1
             for (int d = 0; d < D; d += 32) {
-              tmem_load32(t_o + d, x[0]);
-              tmem_loaded(x[0]);
+              uint32_t x[32];
+              tmem_load32(t_o + d, x);
+              tmem_loaded(x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[0][e] = __float_as_uint(__fmul_rn(__uint_as_float(x[0][e]), g));
-              tmem_store32(t_o + d, x[0]);
+              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__fmul_rn(__uint_as_float(x[e]), g));
+              tmem_store32(t_o + d, x);
             }
             tmem_stored();
           }
@@ -506,69 +641,86 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         // before it is taken off; below, one fma does.
         const float top = m == -CUDART_INF_F ? 0.f : m;
         const bool big = __any_sync(kAll, fabsf(top) > 1048576.f);
-        tmem_load32(t_s, x[0]);
-#pragma unroll
-        for (int cnk = 0; cnk < 4; ++cnk) {
-          uint32_t (&y)[32] = x[cnk & 1];
-          tmem_loaded(y);
-          if (cnk < 3) tmem_load32(t_s + (cnk + 1) * 32, x[(cnk + 1) & 1]);
-          uint32_t pk[16];
+        auto weigh = [&](int cnk, uint32_t (&y)[32]) {
+          float* p = reinterpret_cast<float*>(y);
+          float lp[2], f[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const float f = __fmul_rn(inv, fabsf(ks[cnk * 2 + g]));
+            const float2 sc = scale[cnk * 2 + g];
+            f[g] = __fmul_rn(inv, sc.x);
             // log2 of 2^7 scale / vref; far below, the weights vanish in fp16 anyway
-            float lp = __fadd_rn(__fsub_rn(__log2f(fabsf(vs[cnk * 2 + g])), lref), 7.f);
-            lp = lp < -60.f ? -60.f : lp;
-            const float off = __fsub_rn(lp, top);
-            float s16 = 0.f;
-            float p[16];
-            if (big) {
+            const float x = __fadd_rn(__fsub_rn(sc.y, lref), 7.f);
+            lp[g] = x < -60.f ? -60.f : x;
+          }
+          if (big) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                p[e] = exp2_fast(__fadd_rn(
-                    __fsub_rn(__fmul_rn(__uint_as_float(y[g * 16 + e]), f), top), lp));
-            } else {
+            for (int e = 0; e < 32; ++e)
+              p[e] = __fadd_rn(__fsub_rn(__fmul_rn(p[e], f[e >> 4]), top), lp[e >> 4]);
+          } else {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                p[e] = exp2_fast(__fmaf_rn(__uint_as_float(y[g * 16 + e]), f, off));
+            for (int e = 0; e < 32; e += 2) {
+              const float off = __fsub_rn(lp[e >> 4], top);
+              unpair(fma2(pair(p[e], p[e + 1]), pair(f[e >> 4], f[e >> 4]), pair(off, off)), p[e],
+                     p[e + 1]);
             }
-            if (hide) {
-              const int k0 = key + cnk * 32 + g * 16;
-              const int to = none >> (cnk * 2 + g) & 1 ? lo : hi;
+          }
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (!(k0 + e < to && k0 + e >= lo)) p[e] = 0.f;
-            }
-            float s4[4];
+          for (int e = 0; e < 32; ++e) p[e] = exp2_fast(p[e]);
+          if (hide) {
+            const uint32_t vis = visible(cnk);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[e] = vis >> e & 1 ? p[e] : 0.f;
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint64_t s2[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              s4[e] = __fadd_rn(__fadd_rn(p[e], p[e + 4]), __fadd_rn(p[e + 8], p[e + 12]));
-            s16 = __fadd_rn(__fadd_rn(s4[0], s4[1]), __fadd_rn(s4[2], s4[3]));
-            if (s16 != 0.f) sum = __fmaf_rn(s16, exp2_fast(-lp), sum);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pk[g * 8 + e] = half2_bits(p[2 * e], p[2 * e + 1]);
+              s2[e] = add2(pair(p[g * 16 + 4 * e], p[g * 16 + 4 * e + 1]),
+                           pair(p[g * 16 + 4 * e + 2], p[g * 16 + 4 * e + 3]));
+            float s0, s1;
+            unpair(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])), s0, s1);
+            s0 = __fadd_rn(s0, s1);
+            if (s0 != 0.f) sum = __fmaf_rn(s0, exp2_fast(-lp[g]), sum);
           }
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = half2_bits(p[2 * e], p[2 * e + 1]);
           tmem_store16(t_s + cnk * 16, pk);
+        };
+        tmem_load32(t_s, y0);
+#pragma unroll 1
+        for (int cnk = 0; cnk < 4; cnk += 2) {
+          tmem_loaded(y0);
+          tmem_load32(t_s + (cnk + 1) * 32, y1);
+          weigh(cnk, y0);
+          tmem_loaded(y1);
+          if (cnk == 0) tmem_load32(t_s + 64, y0);
+          weigh(cnk + 1, y1);
         }
         tmem_stored();
         tc_fence_before();
         bar_arrive(&sm->p_full[half]);
+        if (fetched) publish_q();
+        seen |= !hide || visible(0) || visible(1) || visible(2) || visible(3);
       }
       if (!ok) break;
       // ---- the row's result
-      ok = bar_wait(&sm->o_full[half], n_o & 1, sm, a.status);
+      ok = bar_wait(&sm->o_full[half], n_o & 1, &sm->failed, a.status);
       if (!__all_sync(kAll, ok)) {
         ok = false;
         break;
       }
       ++n_o;
       tc_fence_after();
+      // every score -inf: a query that is not finite
+      if (seen && sum == 0.f) sum = CUDART_NAN_F;
       const float unit = __fmul_rn(vref, 1.f / kWeightScale);
       const bool whole = begins && ends;
       const float g = whole ? (sum == 0.f ? 0.f : __fdiv_rn(unit, sum)) : unit;
       float* part = a.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kTileRows * (D + 2);
       const int prow = half * 128 + at_row;
-#pragma unroll
+#pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t x[32];
         tmem_load32(t_o + d, x);
@@ -589,31 +741,90 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         if (!whole)
           *reinterpret_cast<float2*>(part + kTileRows * D + prow * 2) = make_float2(m, sum);
         else if (a.lse)
-          a.lse[(req.start + t) * a.Hq + hq] =
+          a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
               sum == 0.f ? -CUDART_INF_F : __fmul_rn(m + log2f(sum), 0.6931471805599453f);
       }
       tc_fence_before();
-    } while (walk.next(a));
+    } while (more);
     if (tid == 0) a.heads[blockIdx.x] = head;
   } else if (warp < kSoftWarps + kConvWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // ================================================================ converters
-    const int ct = tid - 32 * kSoftWarps, col = ct & 7, row_in = ct >> 3;
-    constexpr int kPlanes = D / 64;
+    // A thread takes 16 codes of a key at a time; the lanes of the upper plane store
+    // their two halves in the other order, so that a phase of 8 lanes hits all banks.
+    const int ct = tid - 32 * kSoftWarps;
+    constexpr int kCols = D / 16, kKeys = 32 * kConvWarps / kCols;  // keys of a round
+    const int col = ct % kCols, key_in = ct / kCols;
+    const bool swap = col >= 4;
+    uint32_t n_k = 0, n_raw = 0;
+    bool ok = true;
+    do {
+      const int n_steps = walk.s1 - walk.s0;
+#pragma unroll 1
+      for (int part = 0; part < 4 * n_steps; ++part, ++n_raw) {
+        const int which = part >> 1 & 1, low = part & 1, stage = n_k % kTileStages;
+        const int slot = n_raw % kRawSlots;
+        if (low == 0) ok = bar_wait(&sm->free[which][stage], ((n_k / kTileStages) & 1) ^ 1, &sm->failed, a.status);
+        ok = ok && bar_wait(&sm->raw_full[slot], (n_raw / kRawSlots) & 1, &sm->failed, a.status);
+        if (!__all_sync(kAll, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t from = base + L::kRaw + slot * (kRawKeys * D) + ct * 16;
+        const uint32_t to = base + (which ? L::kV : L::kK) + stage * L::kOperand + low * (kRawKeys * 128) +
+                            (col / 4) * L::kPlane;
+        // a negative scale (no append gives one) goes into the codes' sign
+        const uint32_t neg = sm->negative[n_k % kScaleSlots] >> (which * kGroups + low * 4);
+        uint32_t w[kRawKeys / kKeys][4];
+#pragma unroll
+        for (int i = 0; i < kRawKeys / kKeys; ++i) lds_words<4>(from + i * (kKeys * D), w[i]);
+#pragma unroll
+        for (int i = 0; i < kRawKeys / kKeys; ++i) {
+          const int row = i * kKeys + key_in;
+          const bool minus = neg >> (row >> 4) & 1;
+          const uint2 lo2 = swap ? make_uint2(w[i][2], w[i][3]) : make_uint2(w[i][0], w[i][1]);
+          const uint2 hi2 = swap ? make_uint2(w[i][0], w[i][1]) : make_uint2(w[i][2], w[i][3]);
+          const uint32_t at = to + row * 128;
+          const uint32_t x = (col % 4) * 32 + (swap ? 16 : 0);
+          uint4 y0, y1;
+          if (kBf16 && which == 0) {
+            y0 = codes_to_bf8(lo2, minus);
+            y1 = codes_to_bf8(hi2, minus);
+          } else {
+            const uint32_t sign2 = minus ? kMinus2 : kPlus2, off2 = minus ? kOffMinus2 : kOffPlus2;
+            y0 = codes_to_half8(lo2, sign2, off2);
+            y1 = codes_to_half8(hi2, sign2, off2);
+          }
+          sts16(at + (x ^ ((row & 7) << 4)), y0);
+          sts16(at + ((x ^ 16) ^ ((row & 7) << 4)), y1);
+        }
+        bar_arrive(&sm->raw_free[slot]);
+        if (low) {
+          proxy_fence();
+          bar_arrive(&sm->full[which][stage]);
+          if (which) ++n_k;
+        }
+      }
+    } while (ok && walk.next(a));
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+    if (warp == kLoadWarp) {
+    // ================================================================ loader
+    // Lane g < 8 has 16-key group g of a step: its block id (-1: none, its keys are
+    // hidden), scales, and the copies of its 16 x D codes of K and of V.
     const int bs = 1 << a.bs_log;
-    uint32_t n_k = 0;
+    const int64_t block_bytes = ((int64_t)a.H << a.bs_log) * D;
+    uint32_t n_k = 0, n_raw = 0;
     bool ok = true;
     do {
       const int n_steps = walk.s1 - walk.s0;
       const int32_t* row_table = a.table + (int64_t)walk.b * a.max_blocks;
-      const int8_t* kb = a.k + (((int64_t)walk.h << a.bs_log) + row_in) * D + col * 8;
-      const int8_t* vb = a.v + (((int64_t)walk.h << a.bs_log) + row_in) * D + col * 8;
-      const int64_t block_bytes = ((int64_t)a.H << a.bs_log) * D;
-      const int key0 = walk.range.lo + walk.s0 * kTileKeys;
-      // lane g < 8: block id (-1: none, its keys are hidden) and scales of 16-key group g
+      const int64_t head_at = ((int64_t)walk.h << a.bs_log) * D;
+      const int key0 = walk.range.lo + walk.s0 * kTileKeys + lane * 16;
       auto look_up = [&](int j, int32_t& id, float& ks, float& vs) {
         id = -1;
         ks = vs = 0.f;
-        const int key = key0 + j * kTileKeys + lane * 16;
+        const int key = key0 + j * kTileKeys;
         if (lane < kGroups && j < n_steps && key < walk.range.hi) {
           id = __ldg(row_table + (key >> a.bs_log));
           if (id < 0 || id >= a.num_blocks) {
@@ -625,87 +836,58 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           }
         }
       };
-      auto load = [&](const int8_t* from, int j, int32_t id_l, uint2 (&w)[kGroups][kPlanes]) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const int32_t id = __shfl_sync(kAll, id_l, g);
-          const int key = key0 + j * kTileKeys + g * 16;
-          const int8_t* p = from + id * block_bytes + (key & (bs - 1)) * D;
-#pragma unroll
-          for (int pl = 0; pl < kPlanes; ++pl) {
-            w[g][pl] = make_uint2(0, 0);
-            if (id >= 0) w[g][pl] = __ldg(reinterpret_cast<const uint2*>(p + pl * 64));
-          }
-        }
-      };
-      auto store = [&](uint32_t to, float scale_l, const uint2 (&w)[kGroups][kPlanes]) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          // a negative scale (no append gives one) goes into the codes' sign
-          const bool neg = __shfl_sync(kAll, scale_l, g) < 0.f;
-          const uint32_t sign2 = neg ? kMinus2 : kPlus2, off2 = neg ? kOffMinus2 : kOffPlus2;
-          const int row = g * 16 + row_in;
-          const uint32_t at = to + row * 128 + ((col * 16) ^ ((row & 7) << 4));
-#pragma unroll
-          for (int pl = 0; pl < kPlanes; ++pl) {
-            const uint4 y = codes_to_half8(w[g][pl], sign2, off2);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + pl * L::kPlane), "r"(y.x),
-                         "r"(y.y), "r"(y.z), "r"(y.w)
-                         : "memory");
-          }
-        }
-      };
       int32_t id, id_n;
       float ks, vs, ks_n, vs_n;
-      uint2 wk[kGroups][kPlanes], wv[kGroups][kPlanes];
       look_up(0, id, ks, vs);
-      load(kb, 0, id, wk);
       for (int j = 0; j < n_steps && ok; ++j, ++n_k) {
-        const int stage = n_k % kTileStages;
-        const uint32_t again = ((n_k / kTileStages) & 1) ^ 1;
-        load(vb, j, id, wv);
         look_up(j + 1, id_n, ks_n, vs_n);
-        ok = bar_wait(&sm->k_free[stage], again, sm, a.status);
-        if (!__all_sync(kAll, ok)) {
-          ok = false;
-          break;
-        }
-        store(base + L::kK + stage * L::kOperand, ks, wk);
-        if (warp == kSoftWarps) {
-          const int slot = n_k % kScaleSlots;
-          const uint32_t none = __ballot_sync(kAll, id < 0) & ((1u << kGroups) - 1);
-          if (lane < kGroups) {
-            sm->ks[slot][lane] = ks;
-            sm->vs[slot][lane] = vs;
+        const uint32_t there = __ballot_sync(kAll, id >= 0);
+        const int64_t off = id * block_bytes + head_at + ((key0 + j * kTileKeys) & (bs - 1)) * D;
+        for (int q = 0; q < 4 && ok; ++q, ++n_raw) {
+          const int slot = n_raw % kRawSlots;
+          ok = bar_wait(&sm->raw_free[slot], ((n_raw / kRawSlots) & 1) ^ 1, &sm->failed, a.status);
+          if (!__all_sync(kAll, ok)) {
+            ok = false;
+            break;
           }
-          if (lane == 0) sm->hidden[slot] = none;
+          if (q == 0) {
+            // every reader of this slot's last step is behind: the codes of three steps
+            // before have been converted, so that step's products were issued
+            const int sl = n_k % kScaleSlots;
+            const uint32_t nk = __ballot_sync(kAll, ks < 0.f), nv = __ballot_sync(kAll, vs < 0.f);
+            if (lane < kGroups) sm->scale[sl][lane] = make_float2(fabsf(ks), log2f(fabsf(vs)));
+            float top = lane < kGroups && fabsf(vs) < CUDART_INF_F ? fabsf(vs) : 0.f;
+            top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(top)));
+            if (lane == 0) {
+              sm->top[sl] = top;
+              sm->hidden[sl] = ~there & ((1u << kGroups) - 1);
+              // a negative softmax scale turns the keys' sign too
+              sm->negative[sl] = (a.scale_log2 < 0.f ? ~nk & 0xFF : nk) | nv << kGroups;
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm->scales[sl]);
+          }
+          const uint32_t mine = there >> (q & 1) * 4 & 0xF;
+          if (lane == 0) bar_expect(&sm->raw_full[slot], __popc(mine) * (16 * D));
           __syncwarp();
-          if (lane == 0) bar_arrive(&sm->scales[slot]);
+          if (id >= 0 && (lane >> 2) == (q & 1))
+            copy_bulk(base + L::kRaw + slot * (kRawKeys * D) + (lane & 3) * (16 * D),
+                      (q < 2 ? a.k : a.v) + off, 16 * D, &sm->raw_full[slot]);
         }
-        proxy_fence();
-        bar_arrive(&sm->k_full[stage]);
-        if (j + 1 < n_steps) load(kb, j + 1, id_n, wk);
-        ok = bar_wait(&sm->v_free[stage], again, sm, a.status);
-        if (!__all_sync(kAll, ok)) {
-          ok = false;
-          break;
-        }
-        store(base + L::kV + stage * L::kOperand, vs, wv);
-        proxy_fence();
-        bar_arrive(&sm->v_full[stage]);
         id = id_n;
         ks = ks_n;
         vs = vs_n;
       }
     } while (ok && walk.next(a));
-  } else {
+    } else if (warp == kMmaWarp) {
     // ================================================================ products
     uint32_t n_k = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-    constexpr uint32_t kScores = instruction<kTileKeys, false>(), kOut = instruction<D, true>();
+    constexpr uint32_t kScores = instruction<kTileKeys, false, kBf16>();
+    constexpr uint32_t kOut = instruction<D, true, false>();
     bool ok = true;
     do {
       const int n_steps = walk.s1 - walk.s0;
-      const int64_t rows = walk.req.w * a.G - walk.tile * kTileRows;
+      const int rows = walk.req.w * a.G - walk.tile * kTileRows;
       const int halves = rows > 128 ? 2 : 1;
       if (lane == 0) {
         auto scores = [&](int i, uint32_t step) {
@@ -720,19 +902,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           tc_commit(&sm->s_full[i]);
         };
         for (int i = 0; i < halves && ok; ++i)
-          ok = bar_wait(&sm->q_full[i], n_q[i]++ & 1, sm, a.status);
+          ok = bar_wait(&sm->q_full[i], n_q[i]++ & 1, &sm->failed, a.status);
         if (ok)
-          ok = bar_wait(&sm->k_full[n_k % kTileStages], (n_k / kTileStages) & 1, sm, a.status);
+          ok = bar_wait(&sm->full[0][n_k % kTileStages], (n_k / kTileStages) & 1, &sm->failed, a.status);
         if (ok) {
           tc_fence_after();
           for (int i = 0; i < halves; ++i) scores(i, n_k);
-          tc_commit(&sm->k_free[n_k % kTileStages]);
+          tc_commit(&sm->free[0][n_k % kTileStages]);
         }
         for (int j = 0; j < n_steps && ok; ++j, ++n_k) {
           const int stage = n_k % kTileStages;
-          ok = bar_wait(&sm->v_full[stage], (n_k / kTileStages) & 1, sm, a.status);
+          ok = bar_wait(&sm->full[1][stage], (n_k / kTileStages) & 1, &sm->failed, a.status);
           for (int i = 0; i < halves && ok; ++i) {
-            ok = bar_wait(&sm->p_full[i], n_p[i]++ & 1, sm, a.status);
+            ok = bar_wait(&sm->p_full[i], n_p[i]++ & 1, &sm->failed, a.status);
             if (!ok) break;
             tc_fence_after();
             const uint32_t v = base + L::kV + stage * L::kOperand;
@@ -740,18 +922,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             for (int kk = 0; kk < kTileKeys / 16; ++kk)
               mma_ts(tmem + 256 + i * D, tmem + i * 128 + kk * 8,
                      operand(v + kk * 2048, L::kPlane, 1024), kOut, j > 0 || kk > 0);
-            if (i == halves - 1) tc_commit(&sm->v_free[stage]);
+            if (i == halves - 1) tc_commit(&sm->free[1][stage]);
             if (j == n_steps - 1) {
               tc_commit(&sm->o_full[i]);
             } else {
               if (i == 0) {
                 const uint32_t nx = n_k + 1;
-                ok = bar_wait(&sm->k_full[nx % kTileStages], (nx / kTileStages) & 1, sm, a.status);
+                ok = bar_wait(&sm->full[0][nx % kTileStages], (nx / kTileStages) & 1, &sm->failed, a.status);
                 if (!ok) break;
                 tc_fence_after();
               }
               scores(i, n_k + 1);
-              if (i == halves - 1) tc_commit(&sm->k_free[(n_k + 1) % kTileStages]);
+              if (i == halves - 1) tc_commit(&sm->free[0][(n_k + 1) % kTileStages]);
             }
           }
         }
@@ -759,13 +941,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       ok = __shfl_sync(kAll, (int)ok, 0) != 0;
     } while (ok && walk.next(a));
   }
+  }
   if (!any && tid == 0) {
     const PartHead none = {0, 0, 0, -1};
     a.heads[blockIdx.x] = none;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftWarps + kConvWarps)
+  if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 

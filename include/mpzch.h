@@ -341,7 +341,8 @@ MPZCH_API int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, i
  * [n][q_heads], natural logarithm of the softmax's denominator.  q, out: device
  * [n][q_heads][dim] of type dtype, strides in elements as for mpzch_kv_append.
  * Rows from cu_new[B] on are neither read nor written.  max_new: the caller's
- * bound on a request's rows; it chooses kernels and changes no result.
+ * bound on a request's rows; it chooses kernels and changes no result beyond
+ * rounding.  n * q_heads and max_blocks * block_size stay below 2^31 - 1024.
  * Key positions come through block_table (int32[B][max_blocks]); a block id
  * outside the cache hides its keys (MPZCH_STATUS_BADBLOCK), a length past
  * max_blocks * block_size or a cu_new outside 0..n is cut (MPZCH_STATUS_BADLEN).
