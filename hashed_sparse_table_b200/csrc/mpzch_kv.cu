@@ -239,6 +239,8 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
   a.out = out;
   a.osn = out_stride_n;
   a.osh = out_stride_h;
+  a.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride_n * bytes % 32 == 0 &&
+                  out_stride_h * bytes % 32 == 0;
   a.lse = lse;
   a.status = dev_status;
   a.min_units = 1;

@@ -26,6 +26,7 @@ struct AttendArgs {
   int causal, window;
   void* out;
   int64_t osn, osh;
+  int out_sectors;    // every head of out starts on a 32-byte boundary
   float* lse;
   int32_t* status;
   int min_units;      // units that a warp takes at least

@@ -8,17 +8,14 @@ namespace mpzch_kv {
 constexpr int kTileRows = 256;   // two halves of 128, each with its softmax warpgroup
 constexpr int kTileKeys = 128;   // keys of one step
 constexpr int kGroups = kTileKeys / 16;
-constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kSoftWarps = 16, kConvWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kConvWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kTileThreads = 512;  // four warpgroups; two warps of the last one idle
-// Registers a thread by warpgroup: 2 softmax, converters, the rest.  The launch gives
-// 512 x 128 = 65,536; the split takes 128 x (2 x 152 + 104 + 104) = 65,536.
-constexpr int kSoftRegs = 152, kConvRegs = 104, kRestRegs = 104;
-static_assert(128 * (2 * kSoftRegs + kConvRegs + kRestRegs) <= 65536);
+constexpr int kTileThreads = 32 * (kLoadWarp + 1);
+constexpr int kItems = 4;        // items known ahead
 constexpr int kTileStages = 2;
 constexpr int kScaleSlots = 4;
-constexpr int kRawKeys = 64;     // keys of a raw slot: K low, K high, V low, V high of a step
-constexpr int kRawSlots = 4;
+constexpr int kRawKeys = 64;     // keys of a raw slot; in turn K low, K high, V low, V high
+constexpr int kRawSlots = 3;
 
 // Shared memory: Q [2 halves][D / 64][128 rows][128 B], K and V stages
 // [D / 64][128 keys][128 B], all in the 128-byte swizzle; then the codes as they come,
@@ -32,7 +29,7 @@ struct TileSmem {
   static constexpr int kV = kK + kTileStages * kOperand;
   static constexpr int kRaw = kV + kTileStages * kOperand;
   static constexpr int kSmall = kRaw + kRawSlots * kRawKeys * D;
-  static constexpr int kBytes = kSmall + 2048 + 1024;  // and up to 1 KB to align the base
+  static constexpr int kBytes = kSmall + 6144 + 1024;  // and up to 1 KB to align the base
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -303,23 +300,56 @@ struct TileWalk {
   }
 };
 
+// What the other warps need of an item; steps == 0 ends the list.
+struct TileItem {
+  int b, h, tile, start, w, L;
+  int key0, hi;        // first key of the share's steps; one behind the last key seen
+  int steps;
+  int whole;           // bit 0: the share holds the item's first step, bit 1: its last
+  int last;            // block whose share ends the item
+};
+
 struct TileSmall {
   uint64_t full[2][kTileStages], free[2][kTileStages];  // [K, V]
   uint64_t raw_full[kRawSlots], raw_free[kRawSlots];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scales[kScaleSlots];
+  uint64_t item_full[kItems], item_free[kItems];
   float2 scale[kScaleSlots][kGroups];  // |key scale|, log2 |value scale| of a group
   float top[kScaleSlots];              // largest finite |value scale| of the step
-  uint32_t hidden[kScaleSlots];  // bit g: group g has no block
-  uint32_t negative[kScaleSlots];  // bit g, 8 + g: its key, value scale is negative
-  TileWalk ahead[kSoftWarps];  // the softmax warps' next items
+  uint32_t hidden[kScaleSlots];        // bit g: group g has no block
+  uint32_t negative[kScaleSlots];      // bit g, 8 + g: its key, value scale is negative
+  TileItem items[kItems];
   int32_t failed;
   uint32_t tmem;
   int32_t b;
   int32_t pad;
-  long long units, before;
+  long long before;
   long long sums[kTileThreads / 32];
+  // [half][columns][row], read by the row's other thread; maxima are written again only
+  // behind the next step's barrier, sums behind the next item's
+  float swap_max[2][2][128], swap_sum[2][2][128];
 };
-static_assert(sizeof(TileSmall) <= 2048);
+static_assert(sizeof(TileSmall) <= 6144);
+
+__device__ __forceinline__ bool any_of_256(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %2, 0;\n"
+      "barrier.cta.red.or.pred q, %1, 256, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_256(int id) {
+  asm volatile("barrier.cta.sync %0, 256;" ::"r"(id) : "memory");
+}
+// 8 words of one 32-byte sector.
+__device__ __forceinline__ void store32(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+               "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
 
 // 8 codes (two words) as 16 bytes of bf16, times sign (+-1): 0x4300 | low 7 bits is
 // 128 + low, 0x4300 | bit 7 is 128 or 256, and their difference is the code, exactly.
@@ -354,16 +384,21 @@ constexpr uint32_t kPlus2 = 0x3C003C00u, kMinus2 = 0xBC00BC00u;      // 1, -1
 constexpr uint32_t kOffPlus2 = 0xE480E480u, kOffMinus2 = 0x64806480u;  // -1152, 1152
 
 // One block an SM.  Per step of 128 keys a loader warp brings the codes of K and V into
-// shared memory (bulk copies of 16 tokens, four slots of 64), a converter warpgroup
-// turns them into fp16 operands there (two stages), one thread issues
+// shared memory (bulk copies of 16 tokens, three slots of 64), a converter warpgroup
+// turns them into 16-bit operands there (two stages), one thread issues
 //   S_i = Q_i K^T (i = 0, 1: the two halves of 128 rows), O_i += P_i V
-// with S and O in TMEM, and a warpgroup for each half turns S_i into P_i: a thread is
-// a row.  P_i takes the place of S_i in TMEM as fp16 pairs.  The halves alternate
-// (P_0 V, Q_0 K', P_1 V, Q_1 K'), so that one half's exponentials run under the other's
-// products.  Scales: the score factor holds the key scale (one for 16 keys); the value
-// scale goes into the exponent, p 2^7 scale / vref = 2^(s - m + log2(..)), and the
-// row sum takes it out again once in 16 keys, so neither costs work per element.  O is
-// rescaled only when a row's maximum rises by more than 2^kSlack or vref changes.
+// with S and O in TMEM, and two warpgroups for each half turn S_i into P_i, a thread
+// taking 64 of a row's 128 keys.  P_i takes the place of S_i in TMEM as fp16 pairs.  The
+// halves alternate (P_0 V, Q_0 K', P_1 V, Q_1 K'), so that one half's exponentials run
+// under the other's products.  What bounds it is the chain of one half, its softmax and
+// then its two products.  Scales: the score factor holds the key scale (one for 16
+// keys); the value scale goes into the exponent, p 2^7 scale / vref =
+// 2^(s - m + log2(..)), and the row sum takes it out again once in 16 keys, so neither
+// costs work per element.  O is rescaled only when a row's maximum rises by more than
+// 2^kSlack or vref changes.
+// The loader warp also walks the block's items and hands them to the others.  A wait
+// that runs out marks the launch failed and lets every role run to its end without
+// further waits, so that all named barriers are met.
 template <int D, typename T>
 __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   pdl_enter();
@@ -383,15 +418,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
-    for (int i = 0; i < kTileStages; ++i) {
-      bar_init(&sm->full[0][i], 32 * kConvWarps);
-      bar_init(&sm->full[1][i], 32 * kConvWarps);
-      bar_init(&sm->free[0][i], 1);
-      bar_init(&sm->free[1][i], 1);
-    }
+    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < kTileStages; ++i) {
+        bar_init(&sm->full[w][i], 32 * kConvWarps);
+        bar_init(&sm->free[w][i], 1);
+      }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&sm->q_full[i], 128);
-      bar_init(&sm->p_full[i], 128);
+      bar_init(&sm->q_full[i], 256);
+      bar_init(&sm->p_full[i], 256);
       bar_init(&sm->s_full[i], 1);
       bar_init(&sm->o_full[i], 1);
     }
@@ -399,6 +433,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
     for (int i = 0; i < kRawSlots; ++i) {
       bar_init(&sm->raw_full[i], 1);
       bar_init(&sm->raw_free[i], 32 * kConvWarps);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      bar_init(&sm->item_full[i], 1);
+      bar_init(&sm->item_free[i], kSoftWarps + kConvWarps + 1);
     }
     sm->failed = 0;
     sm->b = -1;
@@ -427,6 +465,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   __syncthreads();
   tc_fence_after();
   long long total = 0, before = 0;
+#pragma unroll 1
   for (int i = 0; i < kWarps; ++i) {
     if (i < warp) before += sm->sums[i];
     total += sm->sums[i];
@@ -435,7 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   if (per < 1) per = 1;
   const long long u0 = per * blockIdx.x, u_end = min(total, u0 + per);
   {
-    // the worker whose requests hold step u0 walks them
+    // the worker whose requests hold unit u0 walks them
     const long long from = by_warp ? before : before + incl - mine;
     const long long to = by_warp ? before + sm->sums[warp] : before + incl;
     if (from <= u0 && u0 < to) {
@@ -460,39 +499,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   }
   __syncthreads();
   const uint32_t tmem = sm->tmem;
-  bool any = u0 < u_end;
-  TileWalk walk;
-  if (any) {
-    walk.start(a, sm->b, u0 - sm->before, u0, u_end);
-    any = walk.s1 > walk.s0;
-  }
+  volatile int32_t* failed = &sm->failed;
 
-  if (!any) {
-    // no steps here
-  } else if (warp < kSoftWarps) {
+  // Item i; false where the wait ran out.
+  auto item_wait = [&](uint32_t i) {
+    return bar_wait(&sm->item_full[i % kItems], (i / kItems) & 1, failed, a.status);
+  };
+  auto item_done = [&](uint32_t i) {  // the warp has read it
+    __syncwarp();
+    if (lane == 0) bar_arrive(&sm->item_free[i % kItems]);
+  };
+
+  if (warp < kSoftWarps) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int half = warp >> 2;
+    const int half = warp >> 3, part = warp >> 2 & 1;
     const int at_row = (warp & 3) * 32 + lane;  // of the half = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + half * 128 + lanes, t_o = tmem + 256 + half * D + lanes;
-    uint32_t n_s = 0, n_o = 0, n_k = 0;  // s_full and o_full phases, steps so far
-    PartHead head = {0, 0, 0, -1};
-    bool ok = true;
-    // The row's queries go into shared memory as they are (products of 16-bit values
-    // with codes are exact), 16 bytes a copy.  The next item's are asked for when the
-    // last scores of this one are there, and so come under its last step.
+    const uint32_t t_s = tmem + half * 128 + part * 64 + lanes;           // 64 scores
+    const uint32_t t_o = tmem + 256 + half * D + part * (D / 2) + lanes;  // D / 2 outputs
     const float inv = fabsf(a.scale_log2);
-    const uint32_t q_at = base + L::kQ + half * L::kOperand + at_row * 128;
-    auto fetch_q = [&](const TileWalk& w) {
+    // The row's queries go into shared memory as they are (products of 16-bit values
+    // with codes are exact), 16 bytes a copy, half of them by each thread of the row.
+    // The next item's are asked for when the last scores of this one are there, and so
+    // come under its last step.
+    auto fetch_q = [&](const TileItem& w) {
       const int row = w.tile * kTileRows + half * 128 + at_row;
-      const bool real = row < w.req.w * a.G;
+      const bool real = row < w.w * a.G;
       const int t = real ? row / a.G : 0;
-      const T* q = static_cast<const T*>(a.q) + (w.req.start + t) * a.qsn +
-                   (w.h * a.G + (real ? row - t * a.G : 0)) * a.qsh;
+      const T* q = static_cast<const T*>(a.q) + (w.start + t) * a.qsn +
+                   (w.h * a.G + (real ? row - t * a.G : 0)) * a.qsh + part * (D / 2);
+      const uint32_t q_at = base + L::kQ + half * L::kOperand + at_row * 128 +
+                            (D == 128 ? part * L::kPlane : 0);
 #pragma unroll
-      for (int d = 0; d < D; d += 8) {
-        const uint32_t to = q_at + (d / 64) * L::kPlane + (((d % 64) * 2) ^ ((at_row & 7) << 4));
+      for (int d = 0; d < D / 2; d += 8) {
+        const uint32_t to = q_at + ((((D == 128 ? 0 : part * 32) + d) * 2) ^ ((at_row & 7) << 4));
         if (real)
           copy16(to, reinterpret_cast<const int8_t*>(q + d));
         else
@@ -500,79 +540,71 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       }
       copies_commit();
     };
-    auto has_rows = [&](const TileWalk& w) {
-      return w.tile * kTileRows + half * 128 < w.req.w * a.G;
+    auto has_rows = [&](const TileItem& w) {
+      return w.steps > 0 && w.tile * kTileRows + half * 128 < w.w * a.G;
     };
     auto publish_q = [&] {
       copies_wait<0>();
       proxy_fence();
       bar_arrive(&sm->q_full[half]);
     };
-    if (has_rows(walk)) {
-      fetch_q(walk);
-      publish_q();
-    }
-    // the next item waits in shared memory: its fields would cost the loop registers
-    TileWalk* ahead = &sm->ahead[warp];
-    if (lane == 0) *ahead = walk;
-    bool more = true;
-    do {
-      __syncwarp();
-      walk = *ahead;
-      const int n_steps = walk.s1 - walk.s0, first_key = walk.range.lo + walk.s0 * kTileKeys;
-      const bool begins = walk.begins(), ends = walk.ends();
-      const Request req = walk.req;
-      const int row0 = walk.tile * kTileRows + half * 128, h = walk.h;
-      if (begins && !ends) {
-        head.b = walk.b;
-        head.h = walk.h;
-        head.tile = walk.tile;
-        head.last = walk.last_block(per);
+    uint32_t n_s = 0, n_o = 0, n_k = 0;  // s_full and o_full phases, steps so far
+    PartHead head = {0, 0, 0, -1};
+    bool asked = false;  // this item's queries are on their way
+    for (uint32_t it = 0;; ++it) {
+      // the 256 threads of a half agree on going on
+      if (any_of_256(1 + half, !item_wait(it))) break;
+      const TileItem item = sm->items[it % kItems];
+      if (item.steps == 0) break;
+      if (!asked && has_rows(item)) {
+        fetch_q(item);
+        publish_q();
       }
-      more = walk.next(a);
-      const bool next_here = more && has_rows(walk);
-      __syncwarp();
-      if (lane == 0) *ahead = walk;
-      __syncwarp();
-      const int rows = req.w * a.G;
-      if (row0 >= rows) {  // this half of the tile is empty
-        n_k += n_steps;
-        if (next_here) {
-          fetch_q(*ahead);
-          publish_q();
-        }
+      item_done(it);
+      const bool begins = item.whole & 1, whole = item.whole == 3;
+      if (begins && !whole) {
+        head.b = item.b;
+        head.h = item.h;
+        head.tile = item.tile;
+        head.last = item.last;
+      }
+      const bool here = has_rows(item);
+      asked = false;
+      const int row = item.tile * kTileRows + half * 128 + at_row;
+      const bool real = row < item.w * a.G;
+      const int t = real ? row / a.G : 0;
+      const int pos = item.L - item.w + t;
+      const int hi = real ? (a.causal ? max(0, min(item.L, pos + 1)) : item.L) : 0;
+      const int lo = window_low(a, pos);
+      if (!here) {  // this half of the tile is empty
+        n_k += item.steps;
         continue;
       }
-      const int row = row0 + at_row;
-      const bool real = row < rows;
-      const int t = real ? row / a.G : 0;
-      const int hq = h * a.G + (real ? row - t * a.G : 0);
-      const int pos = req.L - req.w + t;
-      const int hi = real ? causal_high(a, req, pos) : 0;
-      const int lo = window_low(a, pos);
       float m = -CUDART_INF_F, sum = 0.f;
       bool seen = false;             // a key of this share
       float vref = 0.f, lref = 0.f;  // power of two above the value scales, its log2
-      for (int j = 0; j < n_steps && ok; ++j, ++n_k) {
-        const int key = first_key + j * kTileKeys;
+#pragma unroll 1
+      for (int j = 0; j < item.steps; ++j, ++n_k) {
+        const int key = item.key0 + j * kTileKeys + part * 64;
         const int slot = n_k % kScaleSlots;
-        ok = bar_wait(&sm->scales[slot], (n_k / kScaleSlots) & 1, &sm->failed, a.status) &&
-             bar_wait(&sm->s_full[half], n_s & 1, &sm->failed, a.status);
-        if (!__all_sync(kAll, ok)) {
-          ok = false;
-          break;
-        }
+        bar_wait(&sm->scales[slot], (n_k / kScaleSlots) & 1, failed, a.status);
+        bar_wait(&sm->s_full[half], n_s & 1, failed, a.status);
         ++n_s;
+        __syncwarp();
         tc_fence_after();
-        const bool fetched = j == n_steps - 1 && next_here;
-        if (fetched) fetch_q(*ahead);
-        const float2* scale = sm->scale[slot];
+        if (j == item.steps - 1) {
+          if (item_wait(it + 1) && has_rows(sm->items[(it + 1) % kItems])) {
+            fetch_q(sm->items[(it + 1) % kItems]);
+            asked = true;
+          }
+          __syncwarp();
+        }
+        const float2* scale = &sm->scale[slot][part * 4];
         const float va = sm->top[slot];
-        const uint32_t none = sm->hidden[slot];
+        const uint32_t none = sm->hidden[slot] >> part * 4 & 0xF;
         // does every row of the warp see every key?  (real rows; the others' results
         // are not used)
-        const bool hide =
-            none || __any_sync(kAll, real && (key + kTileKeys > hi || key < lo));
+        const bool hide = none || __any_sync(kAll, real && (key + 64 > hi || key < lo));
         // keys that this row sees: in [lo, hi) and of a block that is there
         auto visible = [&](int cnk) {
           const uint32_t gone = none >> (cnk * 2);
@@ -582,9 +614,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         // ---- largest score.  The loops over 32 keys stay loops: unrolled, the block's
         // roles together overran the instruction cache.
         float mx = -CUDART_INF_F;
-        auto largest = [&](int cnk, uint32_t (&y)[32]) {
+#pragma unroll 1
+        for (int cnk = 0; cnk < 2; ++cnk) {
+          uint32_t y[32];
+          tmem_load32(t_s + cnk * 32, y);
+          tmem_loaded(y);
           if (hide) {
             const uint32_t vis = visible(cnk);
+            seen |= vis != 0;
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = vis >> e & 1 ? y[e] : 0xFF800000u;
           }
@@ -597,20 +634,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             best = fmaxf(best, z[15]);
             if (best > -CUDART_INF_F) mx = fmaxf(mx, __fmul_rn(best, f));
           }
-        };
-        uint32_t y0[32], y1[32];
-        tmem_load32(t_s, y0);
-#pragma unroll 1
-        for (int cnk = 0; cnk < 4; cnk += 2) {
-          tmem_loaded(y0);
-          tmem_load32(t_s + (cnk + 1) * 32, y1);
-          largest(cnk, y0);
-          tmem_loaded(y1);
-          if (cnk == 0) tmem_load32(t_s + 64, y0);
-          largest(cnk + 1, y1);
         }
+        seen |= !hide;
         const bool vup = va > vref;
-        if (__any_sync(kAll, mx > m + kSlack) || vup) {
+        if (any_of_256(1 + half, mx > m + kSlack || vup)) {
+          sm->swap_max[half][part][at_row] = mx;
+          sync_256(1 + half);
+          mx = fmaxf(mx, sm->swap_max[half][part ^ 1][at_row]);
           float beta = 1.f;
           if (vup) {
             const uint32_t e = (__float_as_uint(va) >> 23) + 1;
@@ -626,7 +656,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           if (j > 0) {
             const float g = __fmul_rn(alpha, beta);
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
+            for (int d = 0; d < D / 2; d += 32) {
               uint32_t x[32];
               tmem_load32(t_o + d, x);
               tmem_loaded(x);
@@ -641,7 +671,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         // before it is taken off; below, one fma does.
         const float top = m == -CUDART_INF_F ? 0.f : m;
         const bool big = __any_sync(kAll, fabsf(top) > 1048576.f);
-        auto weigh = [&](int cnk, uint32_t (&y)[32]) {
+#pragma unroll 1
+        for (int cnk = 0; cnk < 2; ++cnk) {
+          uint32_t y[32];
+          tmem_load32(t_s + cnk * 32, y);
           float* p = reinterpret_cast<float*>(y);
           float lp[2], f[2];
 #pragma unroll
@@ -652,6 +685,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             const float x = __fadd_rn(__fsub_rn(sc.y, lref), 7.f);
             lp[g] = x < -60.f ? -60.f : x;
           }
+          tmem_loaded(y);
           if (big) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -687,68 +721,76 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = half2_bits(p[2 * e], p[2 * e + 1]);
           tmem_store16(t_s + cnk * 16, pk);
-        };
-        tmem_load32(t_s, y0);
-#pragma unroll 1
-        for (int cnk = 0; cnk < 4; cnk += 2) {
-          tmem_loaded(y0);
-          tmem_load32(t_s + (cnk + 1) * 32, y1);
-          weigh(cnk, y0);
-          tmem_loaded(y1);
-          if (cnk == 0) tmem_load32(t_s + 64, y0);
-          weigh(cnk + 1, y1);
         }
         tmem_stored();
         tc_fence_before();
         bar_arrive(&sm->p_full[half]);
-        if (fetched) publish_q();
-        seen |= !hide || visible(0) || visible(1) || visible(2) || visible(3);
       }
-      if (!ok) break;
-      // ---- the row's result
-      ok = bar_wait(&sm->o_full[half], n_o & 1, &sm->failed, a.status);
-      if (!__all_sync(kAll, ok)) {
-        ok = false;
-        break;
-      }
+      if (asked) publish_q();
+      // ---- the row's result: the partner's sum, then D / 2 outputs each
+      if (seen && sum == 0.f) sum = CUDART_NAN_F;  // every score -inf: a query that is not finite
+      sm->swap_sum[half][part][at_row] = sum;
+      sync_256(1 + half);
+      const float other = sm->swap_sum[half][part ^ 1][at_row];
+      sum = part ? __fadd_rn(other, sum) : __fadd_rn(sum, other);
+      bar_wait(&sm->o_full[half], n_o & 1, failed, a.status);
       ++n_o;
+      __syncwarp();
       tc_fence_after();
-      // every score -inf: a query that is not finite
-      if (seen && sum == 0.f) sum = CUDART_NAN_F;
+      const int hq = item.h * a.G + (real ? row - t * a.G : 0);
       const float unit = __fmul_rn(vref, 1.f / kWeightScale);
-      const bool whole = begins && ends;
-      const float g = whole ? (sum == 0.f ? 0.f : __fdiv_rn(unit, sum)) : unit;
-      float* part = a.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kTileRows * (D + 2);
+      const float g = whole ? __fdiv_rn(unit, sum) : unit;
       const int prow = half * 128 + at_row;
+      float* out_part = a.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kTileRows * (D + 2) +
+                        prow * D + part * (D / 2);
+      T* out = static_cast<T*>(a.out) + (item.start + t) * a.osn + hq * a.osh + part * (D / 2);
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
+      for (int d = 0; d < D / 2; d += 32) {
         uint32_t x[32];
         tmem_load32(t_o + d, x);
         tmem_loaded(x);
-        float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           // a row that saw no key: 0, whatever the hidden blocks hold
-          o[e] = sum == 0.f ? 0.f : __fmul_rn(__uint_as_float(x[e]), g);
-        if (real) {
-          if (whole)
-            store_row<T>(static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh + d, o);
-          else
-            store_row<float>(part + prow * D + d, o);
+          x[e] = sum == 0.f ? 0u : __float_as_uint(__fmul_rn(__uint_as_float(x[e]), g));
+        if (!real) continue;
+        if (whole) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float lo2 = __uint_as_float(x[2 * e]), hi2 = __uint_as_float(x[2 * e + 1]);
+            if constexpr (kBf16) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(lo2, hi2);
+              y[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            } else {
+              y[e] = half2_bits(lo2, hi2);
+            }
+          }
+          if (a.out_sectors) {
+            store32(out + d, y);
+            store32(out + d + 16, y + 8);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(out + d + 2 * e) = make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) store32(out_part + d + e, x + e);
         }
       }
-      if (real) {
+      if (real && part == 0) {
         if (!whole)
-          *reinterpret_cast<float2*>(part + kTileRows * D + prow * 2) = make_float2(m, sum);
+          *reinterpret_cast<float2*>(out_part - prow * D + kTileRows * D + prow * 2) =
+              make_float2(m, sum);
         else if (a.lse)
-          a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
+          a.lse[(int64_t)(item.start + t) * a.Hq + hq] =
               sum == 0.f ? -CUDART_INF_F : __fmul_rn(m + log2f(sum), 0.6931471805599453f);
       }
       tc_fence_before();
-    } while (more);
+    }
     if (tid == 0) a.heads[blockIdx.x] = head;
-  } else if (warp < kSoftWarps + kConvWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+  } else if (warp < kMmaWarp) {
     // ================================================================ converters
     // A thread takes 16 codes of a key at a time; the lanes of the upper plane store
     // their two halves in the other order, so that a phase of 8 lanes hits all banks.
@@ -757,19 +799,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
     const int col = ct % kCols, key_in = ct / kCols;
     const bool swap = col >= 4;
     uint32_t n_k = 0, n_raw = 0;
-    bool ok = true;
-    do {
-      const int n_steps = walk.s1 - walk.s0;
+    for (uint32_t it = 0;; ++it) {
+      if (!__all_sync(kAll, item_wait(it))) break;
+      const int n_steps = sm->items[it % kItems].steps;
+      item_done(it);
+      if (n_steps == 0) break;
 #pragma unroll 1
-      for (int part = 0; part < 4 * n_steps; ++part, ++n_raw) {
-        const int which = part >> 1 & 1, low = part & 1, stage = n_k % kTileStages;
+      for (int piece = 0; piece < 4 * n_steps; ++piece, ++n_raw) {
+        const int which = piece >> 1 & 1, low = piece & 1, stage = n_k % kTileStages;
         const int slot = n_raw % kRawSlots;
-        if (low == 0) ok = bar_wait(&sm->free[which][stage], ((n_k / kTileStages) & 1) ^ 1, &sm->failed, a.status);
-        ok = ok && bar_wait(&sm->raw_full[slot], (n_raw / kRawSlots) & 1, &sm->failed, a.status);
-        if (!__all_sync(kAll, ok)) {
-          ok = false;
-          break;
-        }
+        if (low == 0)
+          bar_wait(&sm->free[which][stage], ((n_k / kTileStages) & 1) ^ 1, failed, a.status);
+        bar_wait(&sm->raw_full[slot], (n_raw / kRawSlots) & 1, failed, a.status);
         const uint32_t from = base + L::kRaw + slot * (kRawKeys * D) + ct * 16;
         const uint32_t to = base + (which ? L::kV : L::kK) + stage * L::kOperand + low * (kRawKeys * 128) +
                             (col / 4) * L::kPlane;
@@ -805,54 +846,84 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           if (which) ++n_k;
         }
       }
-    } while (ok && walk.next(a));
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
-    if (warp == kLoadWarp) {
+    }
+  } else if (warp == kLoadWarp) {
     // ================================================================ loader
+    TileWalk walk;
+    uint32_t n_items = 0;
+    bool more = u0 < u_end;
+    if (more) {
+      walk.start(a, sm->b, u0 - sm->before, u0, u_end);
+      more = walk.s1 > walk.s0;
+    }
+    auto publish = [&] {  // the walk's item, or the end of the list
+      const int slot = n_items % kItems;
+      bar_wait(&sm->item_free[slot], ((n_items / kItems) & 1) ^ 1, failed, a.status);
+      if (lane == 0) {
+        TileItem* x = &sm->items[slot];
+        x->steps = more ? walk.s1 - walk.s0 : 0;
+        if (more) {
+          x->b = walk.b;
+          x->h = walk.h;
+          x->tile = walk.tile;
+          x->start = walk.req.start;
+          x->w = walk.req.w;
+          x->L = walk.req.L;
+          x->key0 = walk.range.lo + walk.s0 * kTileKeys;
+          x->hi = walk.range.hi;
+          x->whole = (walk.begins() ? 1 : 0) | (walk.ends() ? 2 : 0);
+          x->last = walk.last_block(per);
+        }
+        bar_arrive(&sm->item_full[slot]);
+      }
+      __syncwarp();
+      ++n_items;
+    };
     // Lane g < 8 has 16-key group g of a step: its block id (-1: none, its keys are
     // hidden), scales, and the copies of its 16 x D codes of K and of V.
     const int bs = 1 << a.bs_log;
     const int64_t block_bytes = ((int64_t)a.H << a.bs_log) * D;
     uint32_t n_k = 0, n_raw = 0;
-    bool ok = true;
-    do {
-      const int n_steps = walk.s1 - walk.s0;
-      const int32_t* row_table = a.table + (int64_t)walk.b * a.max_blocks;
-      const int64_t head_at = ((int64_t)walk.h << a.bs_log) * D;
+    publish();
+    for (uint32_t it = 0; more; ++it) {
+      const int b = walk.b, h = walk.h, n_steps = walk.s1 - walk.s0, hi = walk.range.hi;
       const int key0 = walk.range.lo + walk.s0 * kTileKeys + lane * 16;
+      more = walk.next(a);
+      publish();  // the next one, while this one's codes are brought
+      const int32_t* row_table = a.table + (int64_t)b * a.max_blocks;
+      const int64_t head_at = ((int64_t)h << a.bs_log) * D;
       auto look_up = [&](int j, int32_t& id, float& ks, float& vs) {
         id = -1;
         ks = vs = 0.f;
         const int key = key0 + j * kTileKeys;
-        if (lane < kGroups && j < n_steps && key < walk.range.hi) {
+        if (lane < kGroups && j < n_steps && key < hi) {
           id = __ldg(row_table + (key >> a.bs_log));
           if (id < 0 || id >= a.num_blocks) {
             id = -1;
             set_status(a.status, kStBadBlock);
           } else {
-            ks = __ldg(a.ks + (int64_t)id * a.H + walk.h);
-            vs = __ldg(a.vs + (int64_t)id * a.H + walk.h);
+            ks = __ldg(a.ks + (int64_t)id * a.H + h);
+            vs = __ldg(a.vs + (int64_t)id * a.H + h);
           }
         }
       };
       int32_t id, id_n;
       float ks, vs, ks_n, vs_n;
       look_up(0, id, ks, vs);
-      for (int j = 0; j < n_steps && ok; ++j, ++n_k) {
+#pragma unroll 1
+      for (int j = 0; j < n_steps; ++j, ++n_k) {
         look_up(j + 1, id_n, ks_n, vs_n);
         const uint32_t there = __ballot_sync(kAll, id >= 0);
         const int64_t off = id * block_bytes + head_at + ((key0 + j * kTileKeys) & (bs - 1)) * D;
-        for (int q = 0; q < 4 && ok; ++q, ++n_raw) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q, ++n_raw) {
           const int slot = n_raw % kRawSlots;
-          ok = bar_wait(&sm->raw_free[slot], ((n_raw / kRawSlots) & 1) ^ 1, &sm->failed, a.status);
-          if (!__all_sync(kAll, ok)) {
-            ok = false;
-            break;
-          }
+          bar_wait(&sm->raw_free[slot], ((n_raw / kRawSlots) & 1) ^ 1, failed, a.status);
+          __syncwarp();
           if (q == 0) {
-            // every reader of this slot's last step is behind: the codes of three steps
-            // before have been converted, so that step's products were issued
+            // every reader of this slot's last step is behind: keys of the step before
+            // this one have been converted, so the products of the step before that
+            // were issued, and so the weights of the step before those were ready
             const int sl = n_k % kScaleSlots;
             const uint32_t nk = __ballot_sync(kAll, ks < 0.f), nv = __ballot_sync(kAll, vs < 0.f);
             if (lane < kGroups) sm->scale[sl][lane] = make_float2(fabsf(ks), log2f(fabsf(vs)));
@@ -867,8 +938,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             __syncwarp();
             if (lane == 0) bar_arrive(&sm->scales[sl]);
           }
-          const uint32_t mine = there >> (q & 1) * 4 & 0xF;
-          if (lane == 0) bar_expect(&sm->raw_full[slot], __popc(mine) * (16 * D));
+          const uint32_t mine4 = there >> (q & 1) * 4 & 0xF;
+          if (lane == 0) bar_expect(&sm->raw_full[slot], __popc(mine4) * (16 * D));
           __syncwarp();
           if (id >= 0 && (lane >> 2) == (q & 1))
             copy_bulk(base + L::kRaw + slot * (kRawKeys * D) + (lane & 3) * (16 * D),
@@ -878,16 +949,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         ks = ks_n;
         vs = vs_n;
       }
-    } while (ok && walk.next(a));
-    } else if (warp == kMmaWarp) {
+    }
+    // the last copies have landed (again with a limit) before the block may end
+    for (uint32_t i = n_raw < kRawSlots ? 0 : n_raw - kRawSlots; i < n_raw; ++i) {
+      const uint64_t t0 = global_ns();
+      while (!bar_test(&sm->raw_full[i % kRawSlots], (i / kRawSlots) & 1) &&
+             global_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+  } else {
     // ================================================================ products
     uint32_t n_k = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
     constexpr uint32_t kScores = instruction<kTileKeys, false, kBf16>();
     constexpr uint32_t kOut = instruction<D, true, false>();
-    bool ok = true;
-    do {
-      const int n_steps = walk.s1 - walk.s0;
-      const int rows = walk.req.w * a.G - walk.tile * kTileRows;
+    for (uint32_t it = 0;; ++it) {
+      if (!__all_sync(kAll, item_wait(it))) break;
+      const int n_steps = sm->items[it % kItems].steps;
+      const int rows = sm->items[it % kItems].w * a.G - sm->items[it % kItems].tile * kTileRows;
+      item_done(it);
+      if (n_steps == 0) break;
       const int halves = rows > 128 ? 2 : 1;
       if (lane == 0) {
         auto scores = [&](int i, uint32_t step) {
@@ -901,26 +981,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           }
           tc_commit(&sm->s_full[i]);
         };
-        for (int i = 0; i < halves && ok; ++i)
-          ok = bar_wait(&sm->q_full[i], n_q[i]++ & 1, &sm->failed, a.status);
-        if (ok)
-          ok = bar_wait(&sm->full[0][n_k % kTileStages], (n_k / kTileStages) & 1, &sm->failed, a.status);
-        if (ok) {
-          tc_fence_after();
-          for (int i = 0; i < halves; ++i) scores(i, n_k);
-          tc_commit(&sm->free[0][n_k % kTileStages]);
-        }
-        for (int j = 0; j < n_steps && ok; ++j, ++n_k) {
+        for (int i = 0; i < halves; ++i) bar_wait(&sm->q_full[i], n_q[i]++ & 1, failed, a.status);
+        bar_wait(&sm->full[0][n_k % kTileStages], (n_k / kTileStages) & 1, failed, a.status);
+        tc_fence_after();
+        for (int i = 0; i < halves; ++i) scores(i, n_k);
+        tc_commit(&sm->free[0][n_k % kTileStages]);
+#pragma unroll 1
+        for (int j = 0; j < n_steps; ++j, ++n_k) {
           const int stage = n_k % kTileStages;
-          ok = bar_wait(&sm->full[1][stage], (n_k / kTileStages) & 1, &sm->failed, a.status);
-          for (int i = 0; i < halves && ok; ++i) {
-            ok = bar_wait(&sm->p_full[i], n_p[i]++ & 1, &sm->failed, a.status);
-            if (!ok) break;
+          bar_wait(&sm->full[1][stage], (n_k / kTileStages) & 1, failed, a.status);
+#pragma unroll 1
+          for (int i = 0; i < halves; ++i) {
+            bar_wait(&sm->p_full[i], n_p[i]++ & 1, failed, a.status);
             tc_fence_after();
             const uint32_t v = base + L::kV + stage * L::kOperand;
 #pragma unroll
             for (int kk = 0; kk < kTileKeys / 16; ++kk)
-              mma_ts(tmem + 256 + i * D, tmem + i * 128 + kk * 8,
+              mma_ts(tmem + 256 + i * D, tmem + i * 128 + (kk / 4) * 64 + (kk % 4) * 8,
                      operand(v + kk * 2048, L::kPlane, 1024), kOut, j > 0 || kk > 0);
             if (i == halves - 1) tc_commit(&sm->free[1][stage]);
             if (j == n_steps - 1) {
@@ -928,8 +1005,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             } else {
               if (i == 0) {
                 const uint32_t nx = n_k + 1;
-                ok = bar_wait(&sm->full[0][nx % kTileStages], (nx / kTileStages) & 1, &sm->failed, a.status);
-                if (!ok) break;
+                bar_wait(&sm->full[0][nx % kTileStages], (nx / kTileStages) & 1, failed, a.status);
                 tc_fence_after();
               }
               scores(i, n_k + 1);
@@ -938,13 +1014,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           }
         }
       }
-      ok = __shfl_sync(kAll, (int)ok, 0) != 0;
-    } while (ok && walk.next(a));
-  }
-  }
-  if (!any && tid == 0) {
-    const PartHead none = {0, 0, 0, -1};
-    a.heads[blockIdx.x] = none;
+      __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
