@@ -87,10 +87,12 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_commit(uint64_t* b) {
+__device__ __forceinline__ void tc_commit(uint32_t leader, uint64_t* b) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(b))
+      "{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_addr(b)),
+      "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ void proxy_fence() {
@@ -98,29 +100,38 @@ __device__ __forceinline__ void proxy_fence() {
 }
 
 // Operand descriptor, 128-byte swizzle: start address, leading and stride offsets in
-// 16-byte units, version 1.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lead >> 4) & 0x3FFF) << 16 |
-         (uint64_t)((stride >> 4) & 0x3FFF) << 32 | 1ull << 46 | 2ull << 61;
+// 16-byte units, version 1.  The low word moves with the address alone (shared memory
+// ends below 2^18), so the issuing thread spends one addition for each operand.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr, uint32_t lead) {
+  return addr >> 4 | (lead >> 4) << 16;
 }
+__host__ __device__ constexpr uint32_t operand_high(uint32_t stride) { return stride >> 4 | 1u << 14 | 2u << 29; }
 // fp16 x fp16 (bf16 x bf16) -> fp32, M = 128, N columns; B's N index contiguous if
 // kTransposed.
 template <int N, bool kTransposed, bool kBf16>
 __device__ __forceinline__ constexpr uint32_t instruction() {
   return 1u << 4 | (kBf16 ? 1u << 7 | 1u << 10 : 0u) | (kTransposed ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 | (128u >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// Issued by the warp's leader alone, under a predicate: the operands are the same in
+// every lane, so they stay in uniform registers, which a branch for one lane would
+// fill anew for each product (measured: 130 cycles a product instead of the 64 that it
+// takes).
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t high, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.u32 p, %5, 0;\nsetp.ne.u32 q, %6, 0;\n"
+      "mov.b64 x, {%1, %3};\nmov.b64 y, {%2, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(high), "r"(idesc), "r"((uint32_t)add), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t high, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n.reg .pred p, q;\n.reg .b64 y;\nsetp.ne.u32 p, %5, 0;\nsetp.ne.u32 q, %6, 0;\n"
+      "mov.b64 y, {%2, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(high), "r"(idesc), "r"((uint32_t)add), "r"(leader)
       : "memory");
 }
 
@@ -217,7 +228,7 @@ __device__ __forceinline__ TileRange tile_range(const AttendArgs& a, const Reque
 
 // Beginning and ending an item (queries, result) costs a block about as much as this
 // many steps; shares count an item as kItemCost + steps.
-constexpr int kItemCost = 1;
+constexpr int kItemCost = 2;
 
 // Walks the items (request, kv head, row tile) of a block's share of the work, the
 // same way in every warp.  A share that holds only the first kItemCost units of an
@@ -408,7 +419,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   extern __shared__ __align__(16) uint8_t s_tile[];
   const uint32_t base = (smem_addr(s_tile) + 1023) & ~1023u;
   TileSmall* sm = reinterpret_cast<TileSmall*>(s_tile + (base - smem_addr(s_tile)) + L::kSmall);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // through a shuffle, so that the compiler knows it to be the same in all lanes
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kAll, tid >> 5, 0);
   constexpr int kWarps = kTileThreads / 32;
 
   if (warp == kMmaWarp) {
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
     }
   }
   __syncthreads();
-  const uint32_t tmem = sm->tmem;
+  const uint32_t tmem = __shfl_sync(kAll, sm->tmem, 0);
   volatile int32_t* failed = &sm->failed;
 
   // Item i; false where the wait ran out.
@@ -960,32 +972,37 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   } else {
     // ================================================================ products
     uint32_t n_k = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    const uint32_t leader = lane == 0;
     constexpr uint32_t kScores = instruction<kTileKeys, false, kBf16>();
     constexpr uint32_t kOut = instruction<D, true, false>();
+    constexpr uint32_t kHigh = operand_high(1024);
     for (uint32_t it = 0;; ++it) {
       if (!__all_sync(kAll, item_wait(it))) break;
-      const int n_steps = sm->items[it % kItems].steps;
-      const int rows = sm->items[it % kItems].w * a.G - sm->items[it % kItems].tile * kTileRows;
+      const int n_steps = __shfl_sync(kAll, sm->items[it % kItems].steps, 0);
+      const int rows = __shfl_sync(
+          kAll, sm->items[it % kItems].w * a.G - sm->items[it % kItems].tile * kTileRows, 0);
       item_done(it);
       if (n_steps == 0) break;
       const int halves = rows > 128 ? 2 : 1;
-      if (lane == 0) {
+      {
         auto scores = [&](int i, uint32_t step) {
-          const uint32_t q = base + L::kQ + i * L::kOperand;
-          const uint32_t k = base + L::kK + (step % kTileStages) * L::kOperand;
+          const uint32_t q = operand_low(base + L::kQ + i * L::kOperand, 16);
+          const uint32_t k = operand_low(base + L::kK + (step % kTileStages) * L::kOperand, 16);
+          const uint32_t d = tmem + i * 128;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t at = (kk / 4) * L::kPlane + (kk % 4) * 32;
-            mma_ss(tmem + i * 128, operand(q + at, 16, 1024), operand(k + at, 16, 1024), kScores,
-                   kk > 0);
-          }
-          tc_commit(&sm->s_full[i]);
+          for (int pl = 0; pl < D / 64; ++pl)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t at = (pl * L::kPlane + kk * 32) >> 4;
+              mma_ss(leader, d, q + at, k + at, kHigh, kScores, (pl | kk) != 0);
+            }
+          tc_commit(leader, &sm->s_full[i]);
         };
         for (int i = 0; i < halves; ++i) bar_wait(&sm->q_full[i], n_q[i]++ & 1, failed, a.status);
         bar_wait(&sm->full[0][n_k % kTileStages], (n_k / kTileStages) & 1, failed, a.status);
         tc_fence_after();
         for (int i = 0; i < halves; ++i) scores(i, n_k);
-        tc_commit(&sm->free[0][n_k % kTileStages]);
+        tc_commit(leader, &sm->free[0][n_k % kTileStages]);
 #pragma unroll 1
         for (int j = 0; j < n_steps; ++j, ++n_k) {
           const int stage = n_k % kTileStages;
@@ -994,14 +1011,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           for (int i = 0; i < halves; ++i) {
             bar_wait(&sm->p_full[i], n_p[i]++ & 1, failed, a.status);
             tc_fence_after();
-            const uint32_t v = base + L::kV + stage * L::kOperand;
+            const uint32_t v = operand_low(base + L::kV + stage * L::kOperand, L::kPlane);
+            const uint32_t d = tmem + 256 + i * D, p = tmem + i * 128;
 #pragma unroll
             for (int kk = 0; kk < kTileKeys / 16; ++kk)
-              mma_ts(tmem + 256 + i * D, tmem + i * 128 + (kk / 4) * 64 + (kk % 4) * 8,
-                     operand(v + kk * 2048, L::kPlane, 1024), kOut, j > 0 || kk > 0);
-            if (i == halves - 1) tc_commit(&sm->free[1][stage]);
+              mma_ts(leader, d, p + (kk / 4) * 64 + (kk % 4) * 8, v + kk * (2048 >> 4), kHigh, kOut,
+                     kk > 0 || j > 0);
+            if (i == halves - 1) tc_commit(leader, &sm->free[1][stage]);
             if (j == n_steps - 1) {
-              tc_commit(&sm->o_full[i]);
+              tc_commit(leader, &sm->o_full[i]);
             } else {
               if (i == 0) {
                 const uint32_t nx = n_k + 1;
@@ -1009,7 +1027,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
                 tc_fence_after();
               }
               scores(i, n_k + 1);
-              if (i == halves - 1) tc_commit(&sm->free[0][(n_k + 1) % kTileStages]);
+              if (i == halves - 1) tc_commit(leader, &sm->free[0][(n_k + 1) % kTileStages]);
             }
           }
         }
