@@ -34,18 +34,29 @@ bool rows_ok(const void* p, int64_t sn, int64_t sh, int bytes) {
          sn < (1ll << 40) && sh < (1ll << 40);
 }
 
-template <typename T, int D>
+template <typename T, int D, int W>
 int launch_append(const AppendArgs& a, cudaStream_t st) {
-  const void* kern = reinterpret_cast<const void*>(k_kv_append<T, D>);
-  const int64_t warps = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2;
-  return launch(k_kv_append<T, D>, grid_for(warps * 32, 256, resident_blocks(kern, 256, 0)), 256,
+  const void* kern = reinterpret_cast<const void*>(k_kv_append<T, D, W>);
+  const int64_t warps = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2 * W;
+  return launch(k_kv_append<T, D, W>, grid_for(warps * 32, 256, resident_blocks(kern, 256, 0)), 256,
                 st, true, a);
+}
+
+template <typename T, int D>
+int launch_append_warps(const AppendArgs& a, cudaStream_t st) {
+  const int w = append_warps(D, 1 << a.bs_log);
+  if constexpr (append_warps(D, 128) >= 8)
+    if (w == 8) return launch_append<T, D, 8>(a, st);
+  if constexpr (append_warps(D, 128) >= 4)
+    if (w == 4) return launch_append<T, D, 4>(a, st);
+  return w == 2 ? launch_append<T, D, 2>(a, st) : launch_append<T, D, 1>(a, st);
 }
 
 template <typename T>
 int launch_append_dim(const AppendArgs& a, int dim, cudaStream_t st) {
-  return dim == 32 ? launch_append<T, 32>(a, st)
-                   : dim == 64 ? launch_append<T, 64>(a, st) : launch_append<T, 128>(a, st);
+  return dim == 32 ? launch_append_warps<T, 32>(a, st)
+                   : dim == 64 ? launch_append_warps<T, 64>(a, st)
+                               : launch_append_warps<T, 128>(a, st);
 }
 
 int row_workers() { return sm_count() * kRowBlocksPerSm * kRowWarps; }

@@ -219,87 +219,141 @@ struct AppendArgs {
   int32_t* status;
 };
 
-// 16 consecutive values as fp32.
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+  return x;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+  return x;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t x;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+  return x;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
+  return x;
+}
+// 16 consecutive values of a row as they come: 2 (fp32: 4) 16-byte vectors.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]);
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float (&x)[16]) {
+struct Raw16 {
+  static constexpr int kVec = (int)sizeof(T);
+  uint4 v[kVec];
+};
+
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, Raw16<T>& r) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = v.x;
-    x[4 * i + 1] = v.y;
-    x[4 * i + 2] = v.z;
-    x[4 * i + 3] = v.w;
-  }
+  for (int i = 0; i < Raw16<T>::kVec; ++i) r.v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
 }
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  }
-}
-template <>
-__device__ __forceinline__ void load16<__half>(const __half* p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      __half2 h;
-      *reinterpret_cast<uint32_t*>(&h) = w[j];
-      const float2 f = __half22float2(h);
-      x[8 * i + 2 * j] = f.x;
-      x[8 * i + 2 * j + 1] = f.y;
-    }
+
+// Values 2i and 2i + 1.
+template <typename T>
+__device__ __forceinline__ uint64_t raw_pair(const Raw16<T>& r, int i) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
+  if constexpr (sizeof(T) == 4) {
+    return pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  } else if constexpr (__is_same(T, __nv_bfloat16)) {
+    return pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    return pair(f.x, f.y);
   }
 }
 
-// max of |x| as bit patterns: for non-negative floats the order of the bits is
-// the order of the values, with every NaN above infinity.
-__device__ __forceinline__ uint32_t absmax16(const float (&x)[16], uint32_t a) {
+// Largest |x| so far, as the bits of an fp32 (a) or of two 16-bit numbers: for
+// non-negative floats the order of the bits is the order of the values, with every NaN
+// above infinity.
+template <typename T>
+__device__ __forceinline__ uint32_t absmax_raw(const Raw16<T>& r, uint32_t a) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    a = b > a ? b : a;
-  }
+  for (int i = 0; i < 4 * Raw16<T>::kVec; ++i)
+    a = sizeof(T) == 4 ? max(a, w[i] & 0x7FFFFFFFu) : __vmaxu2(a, w[i] & 0x7FFF7FFFu);
   return a;
 }
-
-__device__ __forceinline__ uint4 codes16(const float (&x)[16], float s, float rcp, bool usable) {
-  int t[16];
-  if (usable) {
-    quant_lane<16>(x, s, rcp, isfinite(rcp), t);
+// The same as an fp32.
+template <typename T>
+__device__ __forceinline__ float absmax_value(uint32_t a) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(a);
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = 0;
+    const uint32_t top = max(a & 0xFFFFu, a >> 16);
+    if constexpr (__is_same(T, __nv_bfloat16)) return __uint_as_float(top << 16);
+    return __half2float(__ushort_as_half((unsigned short)top));
   }
-  return make_uint4(pack4(t[0], t[1], t[2], t[3]), pack4(t[4], t[5], t[6], t[7]),
-                    pack4(t[8], t[9], t[10], t[11]), pack4(t[12], t[13], t[14], t[15]));
 }
 
-// One warp takes rows_per_warp rows of the batch for one head of one cache and
-// works through the runs that begin there.  A lane handles 16 values of a token:
-// 32 * 16 / D tokens a pass.  Values of the first kKeep passes stay in
-// registers between the maximum and the codes; longer runs are read again.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) k_kv_append(AppendArgs a) {
+// rne(fl(x / s)) of 16 values (as pairs).  16-bit inputs lie on the halves between two
+// codes often (x = a / 2 gives 63.5), so the quotient itself is formed, in packed
+// arithmetic: by Markstein's theorem ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990) q' = fma(fma(-q, s, x), rcp, q) with the correctly rounded
+// reciprocal rcp is the correctly rounded quotient when q is within an ulp of it, which
+// the first correction sees to (x rcp is within 1.5).  That needs s in the middle of the
+// exponent range; elsewhere (uniformly for a run) the values are divided.  The integer
+// then comes out of adding 1.5 2^23, in the low byte of the sum.
+__device__ __forceinline__ uint4 codes16(const uint64_t (&x)[8], float s, float rcp) {
+  uint32_t b[16];
+  if (s >= 0x1p-80f && s <= 0x1p100f) {
+    const uint64_t r2 = pair(rcp, rcp), s2 = pair(-s, -s), magic = pair(kRoundMagic, kRoundMagic);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint64_t q = mul2(x[i], r2);
+      q = fma2(fma2(q, s2, x[i]), r2, q);
+      q = fma2(fma2(q, s2, x[i]), r2, q);
+      float lo, hi;
+      unpair(add2(q, magic), lo, hi);
+      b[2 * i] = __float_as_uint(lo);
+      b[2 * i + 1] = __float_as_uint(hi);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float lo, hi;
+      unpair(x[i], lo, hi);
+      b[2 * i] = max(-127, min(127, rne_small(__fdiv_rn(lo, s))));
+      b[2 * i + 1] = max(-127, min(127, rne_small(__fdiv_rn(hi, s))));
+    }
+  }
+  return make_uint4(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]),
+                    pack4(b[8], b[9], b[10], b[11]), pack4(b[12], b[13], b[14], b[15]));
+}
+
+// A group of W warps takes rows_per_warp rows of the batch for one head of one cache and
+// works through the runs that begin there.  A lane handles 16 values of a token, a warp
+// 4 x 32 * 16 / D tokens, all of its loads in flight together; W is what a whole block
+// of tokens needs, so every value is read once and waits in registers for the maximum.
+constexpr int kAppendKeep = 4;
+__host__ __device__ constexpr int append_warps(int D, int bs) {
+  return bs * D / 512 / kAppendKeep > 1 ? bs * D / 512 / kAppendKeep : 1;
+}
+
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
   pdl_enter();
-  constexpr int kLanes = D / 16, kTok = 32 / kLanes, kKeep = 4;
-  const int lane = threadIdx.x & 31, bs = 1 << a.bs_log;
-  const int sub = lane % kLanes, tok = lane / kLanes;
+  constexpr int kLanes = D / 16, kTok = 32 / kLanes, kKeep = kAppendKeep;
+  __shared__ uint32_t s_max[2][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / W, wi = warp % W;
+  const int bs = 1 << a.bs_log;
+  const int sub = lane % kLanes, tok = wi * (kKeep * kTok) + lane / kLanes;
   const int64_t tasks = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2;
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; task < tasks;
-       task += warps) {
+  const int64_t groups = (int64_t)gridDim.x * (8 / W);
+  uint32_t turn = 0;
+  for (int64_t task = (int64_t)blockIdx.x * (8 / W) + group; task < tasks; task += groups) {
     const int h = (int)(task % a.H);
     const int which = (int)(task / a.H % 2);
     const int64_t row0 = task / a.H / 2 * a.rows_per_warp;
@@ -330,54 +384,58 @@ __global__ void __launch_bounds__(256) k_kv_append(AppendArgs a) {
         if (miss) break;
       }
       const T* p = src + row * sn + h * sh + sub * 16;
-      float x[kKeep][16];
+      Raw16<T> x[kKeep];
       uint32_t amax = 0;
 #pragma unroll
       for (int i = 0; i < kKeep; ++i)
-        if (i * kTok + tok < len) {
-          load16<T>(p + (int64_t)(i * kTok + tok) * sn, x[i]);
-        }
-#pragma unroll
-      for (int i = 0; i < kKeep; ++i)
-        if (i * kTok + tok < len) amax = absmax16(x[i], amax);
-      for (int i = kKeep * kTok + tok; i < len; i += kTok) {
-        float y[16];
-        load16<T>(p + (int64_t)i * sn, y);
-        amax = absmax16(y, amax);
-      }
-      amax = __reduce_max_sync(kAll, amax);
+        if (i * kTok + tok < len) load_raw(p + (int64_t)(i * kTok + tok) * sn, x[i]);
       float* sp = scale + blk * a.H + h;
       const float before = o > 0 ? *sp : 0.f;
-      const float own = __fdiv_rn(__uint_as_float(amax), 127.0f);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (i * kTok + tok < len) amax = absmax_raw(x[i], amax);
+      float top = absmax_value<T>(amax);  // not negative: its bits are in order
+      top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(top)));
+      if constexpr (W > 1) {
+        // the slot of two runs ago has been read by every warp: this barrier was between
+        uint32_t* s = s_max[turn++ & 1];
+        if (lane == 0) s[warp] = __float_as_uint(top);
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
+        uint32_t t = s[group * W];
+#pragma unroll
+        for (int i = 1; i < W; ++i) t = max(t, s[group * W + i]);
+        top = __uint_as_float(t);
+      }
+      const float own = __fdiv_rn(top, 127.0f);
       // the larger one; a NaN on either side stays
       const float s = own != own ? own : (before >= own || before != before) ? before : own;
       const bool usable = s > 0.f && s < CUDART_INF_F;
       const float rcp = usable ? __frcp_rn(s) : 0.f;
       int8_t* base = cache + (blk * a.H + h) * ((int64_t)bs * D) + sub * 16;
       if (o > 0 && s != before && (s == s || before == before)) {
-        for (int i = tok; i < o; i += kTok) {
+        for (int i = wi * kTok + lane / kLanes; i < o; i += W * kTok) {
           uint4* c = reinterpret_cast<uint4*>(base + (int64_t)i * D);
           const uint4 v = *c;
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          float y[16];
+          uint64_t y[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            y[j] = __fmul_rn((float)(int8_t)(w[j / 4] >> (8 * (j % 4))), before);
-          *c = codes16(y, s, rcp, usable);
+          for (int j = 0; j < 8; ++j)
+            y[j] = pair(__fmul_rn((float)(int8_t)(w[j / 2] >> (16 * (j % 2))), before),
+                        __fmul_rn((float)(int8_t)(w[j / 2] >> (16 * (j % 2) + 8)), before));
+          *c = usable ? codes16(y, s, rcp) : make_uint4(0, 0, 0, 0);
         }
       }
 #pragma unroll
       for (int i = 0; i < kKeep; ++i)
-        if (i * kTok + tok < len)
+        if (i * kTok + tok < len) {
+          uint64_t y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = raw_pair(x[i], j);
           *reinterpret_cast<uint4*>(base + (int64_t)(o + i * kTok + tok) * D) =
-              codes16(x[i], s, rcp, usable);
-      for (int i = kKeep * kTok + tok; i < len; i += kTok) {
-        float y[16];
-        load16<T>(p + (int64_t)i * sn, y);
-        *reinterpret_cast<uint4*>(base + (int64_t)(o + i) * D) = codes16(y, s, rcp, usable);
-      }
-      __syncwarp();
-      if (lane == 0) *sp = s;
+              usable ? codes16(y, s, rcp) : make_uint4(0, 0, 0, 0);
+        }
+      __syncwarp();  // every lane has read the old scale (W > 1: and every warp)
+      if (wi == 0 && lane == 0) *sp = s;
     }
   }
 }

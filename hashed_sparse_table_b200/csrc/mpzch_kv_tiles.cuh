@@ -175,35 +175,6 @@ __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t x;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
-  return x;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t x;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
-  return x;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t x;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
-  return x;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t x;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
-  return x;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float x;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(x) : "f"(a), "f"(b), "f"(c));
-  return x;
-}
 // Bits of the keys k0 .. k0 + 31 that lie in [lo, hi).
 __device__ __forceinline__ uint32_t keys_between(int k0, int lo, int hi) {
   const int from = max(0, lo - k0), to = min(32, hi - k0);

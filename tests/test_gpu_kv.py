@@ -217,6 +217,32 @@ def test_append_zeros_nan_infinities_and_subnormals(kv):
     run_append(kv, k, v, slots, kc, vc, ks, vs, "fp32")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_append_halves_between_two_codes(kv, kind):
+    """Values whose quotient by the scale lies on a half or a rounding away from one, for block
+    maxima over the whole exponent range of the type."""
+    rng = np.random.default_rng(6)
+    H, D, bs, blocks = 1, 128, 16, 300
+    low, high = {"bf16": (-126, 120), "fp16": (-14, 15), "fp32": (-126, 120)}[kind]
+    top = np.ldexp(1 + rng.random(blocks), rng.integers(low, high, blocks)).astype(np.float32)
+    top = torch.from_numpy(top).to(TYPES[kind]).float().numpy()
+    x = np.zeros((blocks, bs, H, D), np.float32)
+    scale = top / np.float32(127)
+    half = (rng.integers(-127, 127, x.shape) + 0.5).astype(np.float32)
+    with np.errstate(over="ignore", under="ignore"):
+        x = half * scale[:, None, None, None]
+        off = rng.integers(-2, 3, x.shape)
+        x = (x.view(np.int32) + np.where(x != 0, off, 0).astype(np.int32)).view(np.float32)
+    x = np.clip(x, -top[:, None, None, None], top[:, None, None, None])
+    x[:, 0, 0, 0] = top
+    # and halves by construction: powers of two below the maximum
+    x[:, 1, 0] = top[:, None] * np.ldexp(1.0, -rng.integers(0, 9, D)).astype(np.float32)
+    x = x.reshape(blocks * bs, H, D)
+    kc, ks = make_cache(rng, blocks, H, bs, D)
+    slots = np.arange(blocks * bs, dtype=np.int64)
+    run_append(kv, x, -x[::-1].copy(), slots, kc, kc.copy(), ks, ks.copy(), kind)
+
+
 def test_append_skips_bad_slots(kv):
     rng = np.random.default_rng(5)
     H, D, bs = 1, 128, 16
