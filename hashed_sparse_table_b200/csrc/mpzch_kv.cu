@@ -37,9 +37,12 @@ bool rows_ok(const void* p, int64_t sn, int64_t sh, int bytes) {
 template <typename T, int D, int W>
 int launch_append(const AppendArgs& a, cudaStream_t st) {
   const void* kern = reinterpret_cast<const void*>(k_kv_append<T, D, W>);
-  const int64_t warps = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2 * W;
-  return launch(k_kv_append<T, D, W>, grid_for(warps * 32, 256, resident_blocks(kern, 256, 0)), 256,
-                st, true, a);
+  // blocks for one head and cache: for all rows, or for what is resident
+  const int64_t groups = (a.n + a.rows_per_warp - 1) / a.rows_per_warp;
+  int64_t y = (groups + 8 / W - 1) / (8 / W);
+  const int64_t most = (int64_t)sm_count() * resident_blocks(kern, 256, 0) / (2 * a.H);
+  if (y > most) y = most < 1 ? 1 : most;
+  return launch(k_kv_append<T, D, W>, dim3(2 * a.H, (unsigned)y), 256, st, true, a);
 }
 
 template <typename T, int D>

@@ -350,17 +350,17 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp / W, wi = warp % W;
   const int bs = 1 << a.bs_log;
   const int sub = lane % kLanes, tok = wi * (kKeep * kTok) + lane / kLanes;
-  const int64_t tasks = (a.n + a.rows_per_warp - 1) / a.rows_per_warp * a.H * 2;
-  const int64_t groups = (int64_t)gridDim.x * (8 / W);
+  // blocks of one head and cache each, so that no task number has to be divided
+  const int h = blockIdx.x >> 1, which = blockIdx.x & 1;
+  const T* __restrict__ src = static_cast<const T*>(which ? a.x[1] : a.x[0]);
+  const int64_t sn = which ? a.sn[1] : a.sn[0];
+  src += h * (which ? a.sh[1] : a.sh[0]) + sub * 16;
+  int8_t* cache = (which ? a.cache[1] : a.cache[0]) + ((int64_t)h << a.bs_log) * D + sub * 16;
+  float* scale = (which ? a.scale[1] : a.scale[0]) + h;
+  const int64_t block_bytes = ((int64_t)a.H << a.bs_log) * D;
   uint32_t turn = 0;
-  for (int64_t task = (int64_t)blockIdx.x * (8 / W) + group; task < tasks; task += groups) {
-    const int h = (int)(task % a.H);
-    const int which = (int)(task / a.H % 2);
-    const int64_t row0 = task / a.H / 2 * a.rows_per_warp;
-    const T* __restrict__ src = static_cast<const T*>(which ? a.x[1] : a.x[0]);
-    const int64_t sn = which ? a.sn[1] : a.sn[0], sh = which ? a.sh[1] : a.sh[0];
-    int8_t* cache = which ? a.cache[1] : a.cache[0];
-    float* scale = which ? a.scale[1] : a.scale[0];
+  for (int64_t row0 = ((int64_t)blockIdx.y * (8 / W) + group) * a.rows_per_warp; row0 < a.n;
+       row0 += (int64_t)gridDim.y * (8 / W) * a.rows_per_warp) {
     const int64_t mine = row0 + lane;
     const bool in = lane < a.rows_per_warp && mine < a.n;
     const long long slot_l = in ? a.slots[mine] : -1;
@@ -383,13 +383,13 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
         len += miss ? __ffs(miss) - 1 : 32;
         if (miss) break;
       }
-      const T* p = src + row * sn + h * sh + sub * 16;
+      const T* p = src + row * sn;
       Raw16<T> x[kKeep];
       uint32_t amax = 0;
 #pragma unroll
       for (int i = 0; i < kKeep; ++i)
         if (i * kTok + tok < len) load_raw(p + (int64_t)(i * kTok + tok) * sn, x[i]);
-      float* sp = scale + blk * a.H + h;
+      float* sp = scale + blk * a.H;
       const float before = o > 0 ? *sp : 0.f;
 #pragma unroll
       for (int i = 0; i < kKeep; ++i)
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
       const float s = own != own ? own : (before >= own || before != before) ? before : own;
       const bool usable = s > 0.f && s < CUDART_INF_F;
       const float rcp = usable ? __frcp_rn(s) : 0.f;
-      int8_t* base = cache + (blk * a.H + h) * ((int64_t)bs * D) + sub * 16;
+      int8_t* base = cache + blk * block_bytes;
       if (o > 0 && s != before && (s == s || before == before)) {
         for (int i = wi * kTok + lane / kLanes; i < o; i += W * kTok) {
           uint4* c = reinterpret_cast<uint4*>(base + (int64_t)i * D);
