@@ -343,7 +343,7 @@ __host__ __device__ constexpr int append_warps(int D, int bs) {
 }
 
 template <typename T, int D, int W>
-__global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) k_kv_append(AppendArgs a) {
   pdl_enter();
   constexpr int kLanes = D / 16, kTok = 32 / kLanes, kKeep = kAppendKeep;
   __shared__ uint32_t s_max[2][8];
@@ -359,12 +359,20 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
   float* scale = (which ? a.scale[1] : a.scale[0]) + h;
   const int64_t block_bytes = ((int64_t)a.H << a.bs_log) * D;
   uint32_t turn = 0;
-  for (int64_t row0 = ((int64_t)blockIdx.y * (8 / W) + group) * a.rows_per_warp; row0 < a.n;
-       row0 += (int64_t)gridDim.y * (8 / W) * a.rows_per_warp) {
+  // slots of this lane's row and of the one before, asked for one round ahead
+  long long slot_n = -1, prev_n = -2;
+  auto ask = [&](int64_t row0) {
     const int64_t mine = row0 + lane;
     const bool in = lane < a.rows_per_warp && mine < a.n;
-    const long long slot_l = in ? a.slots[mine] : -1;
-    const long long prev_l = in && mine > 0 ? a.slots[mine - 1] : -2;
+    slot_n = in ? __ldg(a.slots + mine) : -1;
+    prev_n = in && mine > 0 ? __ldg(a.slots + mine - 1) : -2;
+  };
+  const int64_t stride = (int64_t)gridDim.y * (8 / W) * a.rows_per_warp;
+  int64_t row0 = ((int64_t)blockIdx.y * (8 / W) + group) * a.rows_per_warp;
+  ask(row0);
+  for (; row0 < a.n; row0 += stride) {
+    const long long slot_l = slot_n, prev_l = prev_n;
+    ask(row0 + stride);
     const bool bad = slot_l >= 0 && (slot_l >> a.bs_log) >= a.num_blocks;
     if (bad) set_status(a.status, kStBadBlock);
     unsigned heads = __ballot_sync(
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(256, 2) k_kv_append(AppendArgs a) {
       int len = 0;
       for (int d = 0; d < bs - o; d += 32) {
         const bool next = d + lane < bs - o && row + d + lane < a.n &&
-                          a.slots[row + d + lane] == slot + d + lane;
+                          __ldg(a.slots + row + d + lane) == slot + d + lane;
         const unsigned miss = ~__ballot_sync(kAll, next);
         len += miss ? __ffs(miss) - 1 : 32;
         if (miss) break;
