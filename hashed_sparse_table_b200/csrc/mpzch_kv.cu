@@ -62,7 +62,11 @@ int launch_append_dim(const AppendArgs& a, int dim, cudaStream_t st) {
                                : launch_append_warps<T, 128>(a, st);
 }
 
-int row_workers() { return sm_count() * kRowBlocksPerSm * kRowWarps; }
+// (the join's table of weights holds the parts of all workers)
+int row_workers() {
+  const int n = sm_count() * kRowBlocksPerSm * kRowWarps;
+  return n < kMostParts ? n : kMostParts;
+}
 
 int64_t head_bytes() {
   return (row_workers() * (int64_t)sizeof(PartHead) + 255) / 256 * 256;
@@ -91,10 +95,14 @@ int launch_rows(const AttendArgs& a, cudaStream_t st) {
   if (rc) return rc;
   int per_sm = resident_blocks(kern, 32 * kRowWarps, row_smem(D));
   if (per_sm > kRowBlocksPerSm) per_sm = kRowBlocksPerSm;
-  const unsigned grid = (unsigned)(sm_count() * per_sm);
+  unsigned grid = (unsigned)(sm_count() * per_sm);
+  if (grid > (unsigned)row_workers() / kRowWarps) grid = row_workers() / kRowWarps;
   rc = launch_smem(k_kv_rows<D, T, R, NQ, NP>, grid, 32 * kRowWarps, row_smem(D), st, true, a);
+  // Items cut into many parts want a block for each row, and there are only a few of
+  // them; where there are many items, most blocks have nothing to join or a few parts,
+  // and the rows of those take a warp each of one block.
   const int64_t rows = (int64_t)a.max_new * a.G;
-  const int y = rows < 1 ? 1 : rows < 4 ? (int)rows : 4;
+  const int y = (int64_t)a.B * a.H > 64 ? 1 : rows < 1 ? 1 : rows < R ? (int)rows : R;
   if (!rc)
     rc = launch(k_kv_join<D, T, R>, dim3(grid * kRowWarps, y), 32 * kJoinWarps, st, true, a);
   return rc;

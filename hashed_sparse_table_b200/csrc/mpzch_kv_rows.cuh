@@ -675,58 +675,88 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
 }
 
 // Joins the parts of the items that k_kv_rows or k_kv_tiles split.  Blocks (i, .) take
-// the item that begins in worker i's share there and goes on into the next ones.
-// With few parts every row gets a warp; with many, block (i, y) takes rows y,
-// y + gridDim.y, .. and its warps take every kJoinWarps-th part, the loads of a round
-// in flight together, and meet in shared memory.  All sums have a fixed order.
-constexpr int kJoinWarps = 8;
+// the item that begins in worker i's share there and goes on into the next ones.  With
+// few parts every row gets a warp; with many, block (i, y) takes rows y, y + gridDim.y,
+// .. and its warps take every kJoinWarps-th part.  The weights of all parts come first
+// (one load a lane), so the parts' loads do not wait for one another.  All sums have a
+// fixed order.
+constexpr int kJoinWarps = 8, kFewParts = 32, kMostParts = 2368;
 template <int D, typename T, int R>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(AttendArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a) {
   pdl_enter();
   const PartHead head = a.heads[blockIdx.x];
   if (head.last < 0) return;
   const int first = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool few = head.last - first < 16;
-  const Request req = request_of(a, head.b, false);
-  __shared__ float s_o[kJoinWarps][D];
-  constexpr int kPer = D / 32, kRound = 8;
-  constexpr int64_t kPart = (int64_t)R * (D + 2);
-  const float* own = a.parts + ((int64_t)first * 2 + 1) * kPart;
-  auto part = [&](int i) { return i == first ? own : a.parts + (int64_t)i * 2 * kPart; };
+  const int parts = head.last - first + 1;
+  const bool few = parts <= kFewParts;
   const int step = few ? 1 : kJoinWarps, rows_at_once = few ? kJoinWarps * gridDim.y : gridDim.y;
-  for (int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y; row < R; row += rows_at_once) {
+  int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
+  if (row >= R) return;
+  const Request req = request_of(a, head.b, false);
+  __shared__ float s_w[kMostParts];       // weights of many parts
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float s_r[2][kJoinWarps];
+  constexpr int kPer = D / 32, kRound = 4;
+  constexpr int64_t kPart = (int64_t)R * (D + 2);
+  const float* all = a.parts + (int64_t)first * 2 * kPart;
+  // part i: the first one is what its worker began, the others what theirs go on with
+  auto part = [&](int i) { return all + (i ? (int64_t)i * 2 : 1) * kPart; };
+  // weight of a part; a part without a key has l = 0, one of NaN alone m = -inf
+  auto weight = [&](float2 ml, float M) {
+    return ml.y == 0.f ? 0.f : ml.x == -CUDART_INF_F ? 1.f : exp2_fast(ml.x - M);
+  };
+  for (; row < R; row += rows_at_once) {
     const int at = head.tile * R + row;
     if (at >= req.w * a.G) return;
-    float M = -CUDART_INF_F;
-    for (int i = first + lane; i <= head.last; i += 32) M = fmaxf(M, part(i)[R * D + row * 2]);
+    auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(part(i) + R * D + row * 2); };
+    float M = -CUDART_INF_F, L = 0.f, mine = 0.f;
+    if (few) {
+      const float2 ml = lane < parts ? ml_of(lane) : make_float2(-CUDART_INF_F, 0.f);
+      M = ml.x;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
-    // weight of a part; a part without a key has l = 0, one of NaN alone m = -inf
-    auto weight = [&](float m, float l) {
-      return l == 0.f ? 0.f : m == -CUDART_INF_F ? 1.f : exp2_fast(m - M);
-    };
-    float L = 0.f;
-    for (int i = first + lane; i <= head.last; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(part(i) + R * D + row * 2);
-      L = __fmaf_rn(ml.y, weight(ml.x, ml.y), L);
+      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
+      mine = weight(ml, M);
+      L = ml.y == 0.f ? 0.f : __fmul_rn(ml.y, mine);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
+    } else {
+      for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) {
+        s_w[i] = ml_of(i).x;
+        M = fmaxf(M, s_w[i]);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
+      if (lane == 0) s_r[0][warp] = M;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_r[0][w]);
+      for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) {
+        const float l = ml_of(i).y, e = weight(make_float2(s_w[i], l), M);
+        s_w[i] = e;
+        if (l != 0.f) L = __fmaf_rn(l, e, L);
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
+      if (lane == 0) s_r[1][warp] = L;
+      __syncthreads();
+      L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) L = __fadd_rn(L, s_r[1][w]);
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
     float o[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) o[k] = 0.f;
-    for (int i0 = first + (few ? 0 : warp); i0 <= head.last; i0 += step * kRound) {
+    for (int i0 = few ? 0 : warp; i0 < parts; i0 += step * kRound) {
       float x[kRound][kPer], e[kRound];
 #pragma unroll
       for (int j = 0; j < kRound; ++j) {
         const int i = i0 + j * step;
-        e[j] = 0.f;
-        if (i <= head.last) {
-          const float* p = part(i);
-          const float2 ml = *reinterpret_cast<const float2*>(p + R * D + row * 2);
+        e[j] = few ? __shfl_sync(kAll, mine, i & 31) : i < parts ? s_w[i] : 0.f;
+        if (i >= parts) e[j] = 0.f;
+        if (i < parts) {
+          const float* p = part(i) + row * D + lane;
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) x[j][k] = p[row * D + lane + 32 * k];
-          e[j] = weight(ml.x, ml.y);
+          for (int k = 0; k < kPer; ++k) x[j][k] = p[32 * k];
         }
       }
 #pragma unroll
@@ -745,7 +775,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join(AttendArgs a) {
 #pragma unroll
           for (int w = 1; w < kJoinWarps; ++w) o[k] = __fadd_rn(o[k], s_o[w][lane + 32 * k]);
       }
-      __syncthreads();  // s_o is free for the next row
+      __syncthreads();  // the arrays are free for the next row
       if (warp) continue;
     }
     const int t = at / a.G;
