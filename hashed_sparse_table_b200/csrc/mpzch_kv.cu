@@ -88,6 +88,11 @@ int launch_tiles(const AttendArgs& a, cudaStream_t st) {
   return rc;
 }
 
+// Histories up to this long go whole to a warp each: its 32 steps take about as long as
+// the launch that would join the parts of a cut one (8 heads x 4 requests of up to 300
+// keys: WHOLE_FIGURES).
+constexpr int64_t kWholeKeys = 512;
+
 template <int D, typename T, int R, int NQ, int NP>
 int launch_rows(const AttendArgs& a, cudaStream_t st) {
   const void* kern = reinterpret_cast<const void*>(k_kv_rows<D, T, R, NQ, NP>);
@@ -98,6 +103,7 @@ int launch_rows(const AttendArgs& a, cudaStream_t st) {
   unsigned grid = (unsigned)(sm_count() * per_sm);
   if (grid > (unsigned)row_workers() / kRowWarps) grid = row_workers() / kRowWarps;
   rc = launch_smem(k_kv_rows<D, T, R, NQ, NP>, grid, 32 * kRowWarps, row_smem(D), st, true, a);
+  if (a.unit_keys != kUnitKeys) return rc;  // no item is cut
   // Items cut into many parts want a block for each row, and there are only a few of
   // them; where there are many items, most blocks have nothing to join or a few parts,
   // and the rows of those take a warp each of one block.
@@ -265,7 +271,7 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
                   out_stride_h * bytes % 32 == 0;
   a.lse = lse;
   a.status = dev_status;
-  a.min_units = 1;
+  a.unit_keys = (int64_t)max_blocks * block_size <= kWholeKeys ? 1 << 30 : kUnitKeys;
   a.max_new = max_new;
   a.heads = static_cast<PartHead*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + head_bytes());

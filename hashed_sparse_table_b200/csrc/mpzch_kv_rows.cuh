@@ -29,7 +29,7 @@ struct AttendArgs {
   int out_sectors;    // every head of out starts on a 32-byte boundary
   float* lse;
   int32_t* status;
-  int min_units;      // units that a warp takes at least
+  int unit_keys;      // keys of one unit of work: kUnitKeys, or all of an item
   int max_new;        // the caller's bound on a request's rows: sizes the join's grid
   struct PartHead* heads;
   float* parts;       // [warp][2]: [R][D] outputs, [R][2] maxima and sums
@@ -78,7 +78,7 @@ __device__ __forceinline__ int first_key(const AttendArgs& a, const Request& r) 
 // number, at least one.
 __device__ __forceinline__ int item_units(const AttendArgs& a, const Request& r) {
   const int keys = r.L - first_key(a, r);
-  return keys > kUnitKeys ? (keys + kUnitKeys - 1) / kUnitKeys : 1;
+  return keys > a.unit_keys ? (keys + a.unit_keys - 1) / a.unit_keys : 1;
 }
 
 template <int R>
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
   const long long total = s_upto[32 * kRowWarps - 1];
   const long long workers = (long long)gridDim.x * kRowWarps;
   long long per = (total + workers - 1) / workers;
-  if (per < a.min_units) per = a.min_units;
+  if (per < 1) per = 1;
   long long u = per * worker;
   const long long u_end = min(total, u + per);
   PartHead head = {0, 0, 0, -1};
@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
     const int any_hi = causal_high(a, req, p_hi), any_lo = window_low(a, p_lo);
     const int all_hi = causal_high(a, req, p_lo), all_lo = window_low(a, p_hi);
     const int key0 = first_key(a, req);
-    const int k_lo = max(key0 + u0 * kUnitKeys, any_lo & ~15);
-    const int k_hi = min(any_hi, key0 + u1 * kUnitKeys);
+    const int k_lo = max(key0 + u0 * a.unit_keys, any_lo & ~15);
+    const int k_hi = (int)min((long long)any_hi, key0 + (long long)u1 * a.unit_keys);
     const int n_steps = k_hi > k_lo ? (k_hi - k_lo + kStepKeys - 1) / kStepKeys : 0;
 
     // Block id and scales of step 32 g + lane: group `c` of the steps that are

@@ -711,11 +711,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       }
       if (asked) publish_q();
       // ---- the row's result: the partner's sum, then D / 2 outputs each
-      if (seen && sum == 0.f) sum = CUDART_NAN_F;  // every score -inf: a query that is not finite
-      sm->swap_sum[half][part][at_row] = sum;
+      // (-0: nothing but weights of 0, from keys that were seen)
+      sm->swap_sum[half][part][at_row] = seen && sum == 0.f ? -0.f : sum;
       sync_256(1 + half);
       const float other = sm->swap_sum[half][part ^ 1][at_row];
-      sum = part ? __fadd_rn(other, sum) : __fadd_rn(sum, other);
+      seen |= __float_as_uint(other) == 0x80000000u;
+      sum = __fadd_rn(fabsf(other), sum);
+      // the largest score has weight 1 at least, so every score was -inf: a query that is
+      // not finite
+      if (seen && sum == 0.f) sum = CUDART_NAN_F;
       bar_wait(&sm->o_full[half], n_o & 1, failed, a.status);
       ++n_o;
       __syncwarp();

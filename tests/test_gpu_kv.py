@@ -307,8 +307,15 @@ def check_attend(c, out, got_lse, scale, causal, window):
     D, kind = got.shape[2], c["kind"]
     nan = np.isnan(want[rows])
     assert np.array_equal(np.isnan(got[rows]), nan)
-    off = np.abs(got - want)[rows]
     bound = ref.attend_bound(want, size, keys, D, kind)[rows]
+    if kind == "fp16":  # results past the type's range (65,520 and up round to infinity)
+        over = np.abs(want[rows]) - bound >= 65520
+        assert (got[rows][over] == np.copysign(np.inf, want[rows][over])).all()
+        edge = over | (np.abs(want[rows]) + bound >= 65504)
+        got, want = got.copy(), want.copy()
+        got[rows] = np.where(edge, 0, got[rows])
+        want[rows] = np.where(edge, 0, want[rows])
+    off = np.abs(got - want)[rows]
     worst = np.nanmax(off / bound, initial=0.0)
     assert worst <= 1.0, worst
     if got_lse is not None:
@@ -358,6 +365,80 @@ def test_attend_many_requests(kv, kind):
     n = 1500
     c = history(8, rng.integers(0, 90, n), rng.integers(0, 3, n), 2, 2, 64, 16, kind)
     run_attend(kv, c)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,H,D,bs", [(2, 2, 64, 16), (5, 1, 128, 32), (4, 2, 128, 128)])
+def test_attend_tiles_cut_over_blocks(kv, kind, Hq, H, D, bs):
+    """Many rows over long histories: items of several row tiles whose steps are shared out over
+    blocks of threads, more and fewer steps than blocks; tiles that end inside their halves."""
+    c = history(31, [6000, 700, 2], [300, 129, 2], Hq, H, D, bs, kind)
+    run_attend(kv, c)
+    run_attend(kv, c, window=900)
+    c = history(32, [30000], [20], Hq, H, D, bs, kind)
+    run_attend(kv, c, causal=False)
+    run_attend(kv, c)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_attend_tiles_of_many_requests(kv, kind):
+    """More requests than threads of a block, most of them short, some without rows or keys."""
+    rng = np.random.default_rng(33)
+    n = 1500
+    new = rng.integers(0, 4, n)
+    new[::97] = rng.integers(20, 150, len(new[::97]))
+    lens = rng.integers(0, 60, n)
+    lens[::50] += 300
+    c = history(33, lens, new, 4, 2, 64, 16, kind)
+    run_attend(kv, c)
+    run_attend(kv, c, causal=False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,D", [(1, 64), (9, 32), (150, 64), (150, 128)])
+def test_attend_negative_and_zero_scales(kv, kind, rows, D):
+    c = history(34, [300, 260], [rows] * 2, 2, 1, D, 16, kind)
+    c["ks"][::3] *= -1
+    c["vs"][1::4] *= -1
+    c["ks"][::5] = 0
+    c["vs"][2::5] = 0
+    run_attend(kv, c)
+    run_attend(kv, c, scale=-0.2, causal=False)
+    c["vs"][:] = 0
+    out, _ = run_attend(kv, c)
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_attend_tiles_scores_far_apart(kv, kind):
+    """Scores of thousands: nearly all weight on one key, weights far below the largest, rows
+    whose maximum rises step by step (the accumulators are rescaled)."""
+    c = history(35, [900], [150], 2, 2, 64, 16, kind)
+    run_attend(kv, c, scale=20.0, causal=False)
+    ids = c["table"][0, :57]
+    c["ks"][ids] = np.float32(0.002) * np.float32(1.12) ** np.arange(57)[:, None]
+    c["vs"][ids] = np.float32(0.01) * np.float32(1.3) ** np.arange(57)[:, None]
+    run_attend(kv, c, scale=0.5)
+    c["vs"][ids] = c["vs"][ids[::-1]]
+    run_attend(kv, c, scale=0.5, causal=False)
+    # scores past 2^20: finite, and a weighted mean of the values
+    q = c["q"].cuda()
+    out = torch.empty_like(q)
+    kv.mpzch_kv_attend(q, dev(c["kc"]), dev(c["vc"]), dev(c["ks"]), dev(c["vs"]), dev(c["table"]),
+                       dev(c["cu"]), dev(c["seq"]), 150, out, softmax_scale=1e9, causal=False)
+    got = out.float()
+    assert got.isfinite().all() and got.abs().max() <= 128 * float(c["vs"].max())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("length", [496, 512, 513, 528])
+def test_attend_around_the_longest_whole_history(kv, kind, length):
+    """Tables that hold up to 512 keys and more: items go whole to a warp, or are cut."""
+    c = history(36, [length, 40, 0, length - 7], [1, 2, 1, 1], 4, 2, 64, 16, kind)
+    for width in (length // 16 + 1, length // 16 + 40):
+        t = np.full((4, width), -1, np.int32)
+        t[:, :min(width, c["table"].shape[1])] = c["table"][:, :width]
+        run_attend(kv, {**c, "table": t})
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
