@@ -272,6 +272,7 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
   a.lse = lse;
   a.status = dev_status;
   a.unit_keys = (int64_t)max_blocks * block_size <= kWholeKeys ? 1 << 30 : kUnitKeys;
+  a.item_cost = a.unit_keys == kUnitKeys ? kRowItemCost : 0;
   a.max_new = max_new;
   a.heads = static_cast<PartHead*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + head_bytes());

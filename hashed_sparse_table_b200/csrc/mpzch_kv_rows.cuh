@@ -8,6 +8,7 @@ namespace mpzch_kv {
 constexpr int kMaxRows = 16;    // query rows (token, head of the group) of a tile: 8 or 16
 constexpr int kUnitKeys = 64;   // keys of one unit of work: four steps of a warp
 constexpr int kStepKeys = 16;
+constexpr int kRowItemCost = 1;  // queries, result and the empty ring, in units
 constexpr int kRowWarps = 4;    // independent warps of a block
 constexpr int kRowBlocksPerSm = 4;
 
@@ -30,6 +31,7 @@ struct AttendArgs {
   float* lse;
   int32_t* status;
   int unit_keys;      // keys of one unit of work: kUnitKeys, or all of an item
+  int item_cost;      // units that the shares count for an item besides its keys
   int max_new;        // the caller's bound on a request's rows: sizes the join's grid
   struct PartHead* heads;
   float* parts;       // [warp][2]: [R][D] outputs, [R][2] maxima and sums
@@ -88,7 +90,7 @@ __device__ __forceinline__ int row_tiles(const AttendArgs& a, const Request& r) 
 
 template <int R>
 __device__ __forceinline__ long long request_units(const AttendArgs& a, const Request& r) {
-  return (long long)(row_tiles<R>(a, r) * a.H) * item_units(a, r);
+  return (long long)(row_tiles<R>(a, r) * a.H) * (item_units(a, r) + a.item_cost);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -317,19 +319,35 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
   const uint32_t ring =
       (uint32_t)__cvta_generic_to_shared(s_ring) + warp * (kSlots * 2 * kTile);
 
+  // Where this lane's chunks go in a staged tile, and where it reads: staged() taken
+  // apart, so that the loop adds one of a few numbers to a slot's address.  Key chunk 1
+  // (D = 128) lies at the flipped bit 6; value rows 2c + 1 at v_at1, rows 8 on 8 rows on;
+  // value chunks of every other group of 4 rows at the flipped bit 6 too.
+  constexpr uint32_t kOdd = D == 128 ? 64 : 0;
+  const uint32_t k_to = staged<D, false>(lane / kCols, lane % kCols);
+  const uint32_t v_to = staged<D, true>(lane / kCols, lane % kCols);
+  const uint32_t k_at = D >= 64 ? staged<D, false>(r, c) : r * D + c * 8;
+  const uint32_t v_at0 = staged<D, true>(2 * c, r * (D / 8) >> 4) + (r * (D / 8) & 15);
+  const uint32_t v_at1 = staged<D, true>(2 * c + 1, r * (D / 8) >> 4) + (r * (D / 8) & 15);
+
   while (u < u_end) {
     const Request req = request_of(a, b, false);
     const int tiles = row_tiles<R>(a, req), units = item_units(a, req);
-    const long long all = (long long)(tiles * a.H) * units;
+    const int cost = units + a.item_cost;
+    const long long all = (long long)(tiles * a.H) * cost;
     if (b_units + all <= u) {
       b_units += all;
       ++b;
       continue;
     }
     const long long into = u - b_units;
-    const int item = (into >> 32) ? (int)(into / units) : (int)((uint32_t)into / (uint32_t)units);
-    const int u0 = (int)(into - (long long)item * units);
-    const int u1 = (int)min((long long)units, u0 + (u_end - u));
+    const int item = (into >> 32) ? (int)(into / cost) : (int)((uint32_t)into / (uint32_t)cost);
+    // the share takes [x0, x1) of the item's cost, which are its units [u0, u1); one that
+    // ends before the first unit leaves the item to the next share
+    const int x0 = (int)(into - (long long)item * cost);
+    const int x1 = (int)min((long long)cost, x0 + (u_end - u));
+    const int u0 = max(0, x0 - a.item_cost), u1 = max(0, x1 - a.item_cost);
+    if (u0 == u1) break;
     const int h = item / tiles, tile = item % tiles;
     const int rows = req.w * a.G, first_row = tile * R;
     const int n_rows = min(R, rows - first_row);
@@ -374,9 +392,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
             (int64_t)id * block_bytes + ((k_lo + s * kStepKeys) & (bs - 1)) * D;
 #pragma unroll
         for (int i = 0; i < kTile / 512; ++i) {
-          const int row = i * (32 / kCols) + lane / kCols, col = lane % kCols;
-          copy16(to + staged<D, false>(row, col), kb + off + i * 512);
-          copy16(to + kTile + staged<D, true>(row, col), vb + off + i * 512);
+          copy16(to + k_to + i * 512, kb + off + i * 512);
+          copy16(to + kTile + (i & 1 ? v_to ^ kOdd : v_to) + i * 512, vb + off + i * 512);
         }
       }
       copies_commit();
@@ -481,21 +498,14 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
       uint32_t kw[2][kK];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = j * 8 + r;
-        if constexpr (D >= 64) {
 #pragma unroll
-          for (int i = 0; i < kChunks; ++i)
-            lds_words<4>(kt + staged<D, false>(row, i * 4 + c), &kw[j][i * 4]);
-        } else {
-          lds_words<2>(kt + row * D + c * 8, kw[j]);
-        }
+        for (int i = 0; i < kChunks; ++i)
+          lds_words<kWK>(kt + (i ? k_at ^ 64 : k_at) + j * 8 * D, &kw[j][i * kWK]);
       }
       uint32_t vw[4][kWV];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int row = 2 * c + (j & 1) + (j >> 1) * 8;
-        const int byte = r * (D / 8);  // of the row
-        lds_words<kWV>(vt + staged<D, true>(row, byte >> 4) + (byte & 15), vw[j]);
+        lds_words<kWV>(vt + (j & 1 ? v_at1 : v_at0) + (j >> 1) * 8 * D, vw[j]);
       }
       float sc[NR][4];  // [rows 8 i ..][2 j + k]: key r + 8 j, row 2c + k
 #pragma unroll
@@ -667,9 +677,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
       head.b = b;
       head.h = h;
       head.tile = tile;
-      head.last = (int)((b_units + (item + 1ll) * units - 1) / per);
+      head.last = (int)((b_units + (item + 1ll) * cost - 1) / per);
     }
-    u += u1 - u0;
+    u += x1 - x0;
   }
   if (lane == 0) a.heads[worker] = head;
 }
