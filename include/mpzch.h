@@ -346,11 +346,15 @@ MPZCH_API int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, i
  * Key positions come through block_table (int32[B][max_blocks]); a block id
  * outside the cache hides its keys (MPZCH_STATUS_BADBLOCK), a length past
  * max_blocks * block_size or a cu_new outside 0..n is cut (MPZCH_STATUS_BADLEN).
- * Arithmetic: scores, maxima, sums and accumulators in fp32.  Products take
- * fp16 operands, the codes exactly and the queries after a power-of-two scaling of
- * the row (F32: in two parts, 22 bits); softmax weights are rounded to fp16
- * (F32: two parts).  A query row with a NaN or an infinity that sees a key gives
- * NaN.  Results do not depend on timing (no float atomics).
+ * Arithmetic: scores, maxima, sums and accumulators in fp32.  Products take 16-bit
+ * operands: the codes exactly; F16 and BF16 queries exactly (below 2^113 in size, past
+ * which a row may give NaN), F32 ones in two parts, 22 bits, after a power-of-two scaling
+ * of the row; softmax weights rounded to fp16 (F32, and F16 with few rows: two parts),
+ * where weights below 2^-21 of the largest lose bits and those below 2^-32 vanish.
+ * Scales may be zero or negative.  A query row with a NaN or an infinity that sees a key
+ * gives NaN; a scale that is NaN gives NaN to the rows that see a key of its block, an
+ * infinite one what infinite scores or values leave; other rows do not notice.  Results
+ * do not depend on timing (no float atomics).
  * workspace: device, 256-byte aligned, mpzch_kv_attend_workspace bytes; calls
  * that may overlap on the device need one each. */
 MPZCH_API int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64_t n,
