@@ -647,7 +647,8 @@ def mpzch_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, 
 
 class MpzchHistory:
     """An int8 history cache (codes and scales as torch tensors) with its list of free blocks and
-    the requests' block tables; methods forward to the entry points above."""
+    the requests' block tables; methods forward to the entry points above, on the current
+    stream (their results come from torch's allocator for it)."""
 
     def __init__(self, num_blocks: int, block_size: int, kv_heads: int, dim: int,
                  max_requests: int, max_blocks: int):
@@ -667,24 +668,24 @@ class MpzchHistory:
     def cache(self):
         return self.k_cache, self.v_cache, self.k_scale, self.v_scale
 
-    def extend(self, new_len, n_slots: int, stream=None):
+    def extend(self, new_len, n_slots: int):
         """Room for new_len[b] more tokens of every request; returns (cu_new, slots)."""
         dev = self.seq_len.device
         cu = torch.empty(new_len.numel() + 1, dtype=torch.int32, device=dev)
         slots = torch.empty(n_slots, dtype=torch.int64, device=dev)
         seq, left = torch.empty_like(self.seq_len), torch.empty_like(self.free_count)
         mpzch_kv_tables(self.seq_len, new_len, self.block_size, self.free_blocks, self.free_count,
-                        self.block_table, cu, seq, slots, left, self.status, stream)
+                        self.block_table, cu, seq, slots, left, self.status)
         self.seq_len, self.free_count = seq, left
         return cu, slots
 
-    def append(self, k, v, slots, stream=None):
-        mpzch_kv_append(k, v, slots, *self.cache(), self.status, stream)
+    def append(self, k, v, slots):
+        mpzch_kv_append(k, v, slots, *self.cache(), self.status)
 
-    def attend(self, q, cu_new, max_new: int, out=None, stream=None, **options):
+    def attend(self, q, cu_new, max_new: int, out=None, **options):
         out = torch.empty_like(q) if out is None else out
         mpzch_kv_attend(q, *self.cache(), self.block_table, cu_new, self.seq_len, max_new, out,
-                        status=self.status, stream=stream, **options)
+                        status=self.status, **options)
         return out
 
 

@@ -14,6 +14,7 @@ using namespace mpzch_internal;
 namespace {
 
 constexpr int64_t kMaxInt = 0x7FFFFFFFll;
+constexpr float kLog2E = 1.4426950408889634f;
 
 int log2_of(int x) {
   int k = 0;
@@ -232,7 +233,8 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
   const int64_t need = mpzch_kv_attend_workspace(q_heads, kv_heads, dim);
   if (need < 0 || bytes == 0 || n < 0 || n > (kMaxInt - 1024) / q_heads || !block_size_ok(block_size) ||
       num_blocks < 0 || num_blocks > kMaxInt || max_blocks < 0 || n_requests < 0 ||
-      n_requests > MPZCH_KV_MAX_REQUESTS || max_new < 0 || !std::isfinite(softmax_scale) ||
+      n_requests > MPZCH_KV_MAX_REQUESTS || max_new < 0 ||
+      !std::isfinite(softmax_scale * kLog2E) ||
       window < 0 || (window > 0 && !causal) ||
       ((int64_t)max_blocks * block_size > kMaxInt - 1024))
     return MPZCH_EINVAL;
@@ -262,7 +264,7 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
   a.cu = cu_new;
   a.seq = seq_len;
   a.B = n_requests;
-  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.scale_log2 = softmax_scale * kLog2E;
   a.causal = causal ? 1 : 0;
   a.window = window;
   a.out = out;

@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(1024) k_kv_tables(TablesArgs a) {
   }
   // new table entries: entry e of those given out belongs to the first request
   // with s_upto > e
-  for (int e = gtid; e < given; e += gthreads) {
-    const int b = first_above(s_upto, served, e);
+  for (int64_t e = gtid; e < given; e += gthreads) {
+    const int b = first_above(s_upto, served, (int)e);
     const int before = b ? s_upto[b - 1] : 0;
     const long long old = ((long long)a.cached[b] + bs - 1) >> a.bs_log;
     a.table[(int64_t)b * a.max_blocks + old + (e - before)] = a.free_blocks[count - 1 - e];

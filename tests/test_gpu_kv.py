@@ -711,6 +711,38 @@ def test_step_captured_and_replayed_on_its_own_stream(kv):
     assert int(h.status) == 0
 
 
+CAPTURE_FIRST = """
+import sys
+sys.path[:0] = [%r, %r]
+import numpy as np, torch
+import kv_ref as ref, test_gpu_kv as t
+from hashed_sparse_table_b200 import binding as kv
+for rows, kind in ((1, "bf16"), (30, "fp16")):
+    c = t.history(40, [700, 90], [rows] * 2, 4, 2, 64, 16, kind)
+    a = [c["q"].cuda()] + [t.dev(c[x]) for x in ("kc", "vc", "ks", "vs", "table", "cu", "seq")]
+    out = torch.full_like(a[0], 7.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kv.mpzch_kv_attend(*a, rows, out)
+    assert (out == 7.0).all()
+    g.replay()
+    torch.cuda.synchronize()
+    t.check_attend(c, out, None, 0.125, True, 0)
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """No call before the capture has loaded the kernels."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    done = subprocess.run([sys.executable, "-c", CAPTURE_FIRST % (os.path.dirname(here), here)],
+                          capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stderr[-2000:]
+
+
 def test_calls_on_two_streams_at_once(kv):
     """Two attention calls in flight together, each with a workspace, one on a raw stream."""
     a = history(22, [5000, 10], [1, 1], 8, 2, 64, 16, "bf16")

@@ -71,7 +71,7 @@ def attend(lib, **change):
     dict(n=-1), dict(n=2**31), dict(dtype=5), dict(bs=17), dict(Hq=5), dict(Hq=0), dict(H=0),
     dict(Hq=8192), dict(D=16), dict(blocks=-1), dict(max_blocks=-1), dict(max_blocks=2**27),
     dict(B=-1), dict(B=16385), dict(max_new=-1), dict(scale=float("inf")),
-    dict(scale=float("nan")), dict(window=-1), dict(window=4, causal=0), dict(q=None),
+    dict(scale=float("nan")), dict(scale=3e38), dict(n=2**31 // 4), dict(window=-1), dict(window=4, causal=0), dict(q=None),
     dict(out=None), dict(cu=None), dict(seq=None), dict(table=None), dict(kc=None), dict(vc=None),
     dict(ks=None), dict(vs=None), dict(ws=None), dict(ws_bytes=100), dict(ws=FAKE + 16),
     dict(q=FAKE + 4), dict(out=FAKE + 8), dict(qsn=250), dict(osh=-64), dict(kc=FAKE + 1)])
