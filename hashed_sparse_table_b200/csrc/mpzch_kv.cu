@@ -85,7 +85,7 @@ int launch_tiles(const AttendArgs& a, cudaStream_t st) {
   int rc = launch_smem(k_kv_tiles<D, T>, grid, kTileThreads, kBytes, st, true, a);
   if (!rc)
     rc = launch(k_kv_join<D, T, kTileRows>, dim3(grid, kTileRows / kJoinWarps), 32 * kJoinWarps, st,
-                true, a);
+                true, a, (int)grid);
   return rc;
 }
 
@@ -108,22 +108,31 @@ int launch_rows(const AttendArgs& a, cudaStream_t st) {
   if (a.unit_keys != kUnitKeys) return rc;  // no item is cut
   // Items cut into many parts want a block for each row, and there are only a few of
   // them; where there are many items, most blocks have nothing to join or a few parts,
-  // and the rows of those take a warp each of one block.
+  // and a warp for every second row of their items is enough (64 x 1..7 drafts, 8 query
+  // heads to a kv head: 21.4 us with R / 4 blocks across, 27.2 with R).
   const int64_t rows = (int64_t)a.max_new * a.G;
-  const int y = (int64_t)a.B * a.H > 64 ? 1 : rows < 1 ? 1 : rows < R ? (int)rows : R;
+  const int y = (int64_t)a.B * a.H > 64 ? R / 4 : rows < 1 ? 1 : rows < R ? (int)rows : R;
   if (!rc)
-    rc = launch(k_kv_join<D, T, R>, dim3(grid * kRowWarps, y), 32 * kJoinWarps, st, true, a);
+    rc = launch(k_kv_join<D, T, R>, dim3((grid * kRowWarps + join_heads<R>() - 1) / join_heads<R>(), y),
+                32 * kJoinWarps, st, true, a, (int)(grid * kRowWarps));
   return rc;
 }
 
-// Tiles of 8 rows where no request has more, else of 16.
+// Tiles of 8 rows where no request has more, else of 16; 16-bit types with more rows go
+// to the tile kernel.  A half tile of it costs the same for 20 rows as for 128, and a
+// block takes one item at a time, so many requests with up to 32 (dim 128) or 64 (dim 64)
+// rows stay here.  Row kernel against tile kernel, us on the device: 64 requests x 8 kv
+// heads x 20 rows, dim 128, up to 512 keys 35 : 50; 128 x 2 x 32 rows, dim 128, 1,000 to 4,000
+// keys 89 : 112; 64 x 2 x 56 rows, dim 64, window 1,024 21 : 29, all of up to 8,192 keys
+// 36 : 38; but 32 x 2 x 32 rows, dim 128 42 : 39; 16 x 8 x 32 rows, up to 512 keys 39 : 25;
+// 8 x 2 x 20 rows, up to 1,000 keys 24 : 17.
 template <int D, typename T, int NQ, int NP>
 int launch_rows(const AttendArgs& a, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.max_new * a.G;
   if constexpr (D >= 64 && sizeof(T) == 2) {
-    if ((int64_t)a.max_new * a.G > 16) return launch_tiles<D, T>(a, st);
+    if (rows > 16 && (a.B < 64 || rows * D > 4096)) return launch_tiles<D, T>(a, st);
   }
-  return (int64_t)a.max_new * a.G <= 8 ? launch_rows<D, T, 8, NQ, NP>(a, st)
-                                       : launch_rows<D, T, 16, NQ, NP>(a, st);
+  return rows <= 8 ? launch_rows<D, T, 8, NQ, NP>(a, st) : launch_rows<D, T, 16, NQ, NP>(a, st);
 }
 
 template <typename T, int NQ, int NP>

@@ -244,7 +244,7 @@ __device__ __forceinline__ void store_row(T* p, const float (&x)[N]) {
 // (turning a byte into fp16 is one byte permutation and one subtraction for two): 256
 // tokens, 32 query and 8 kv heads x 128, 515 MB of cache, 108 us with the join, 4.8 TB/s,
 // 0.73 of the measured copy rate; two histories of 78 and 110 thousand keys, 4 kv heads x
-// 128, fp16, 193 MB, 51 us; 4,096 fp32 histories of up to 1,000 keys, 4 heads x 128, 625 MB,
+// 128, fp16, 193 MB, 48 us; 4,096 fp32 histories of up to 1,000 keys, 4 heads x 128, 625 MB,
 // 201 us (two products for each, and half of the time in beginning and ending items).
 template <int D, typename T, int R, int NQ, int NP>
 __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : NQ == 1 ? 3 : 2)
@@ -691,54 +691,122 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
   if (lane == 0) a.heads[worker] = head;
 }
 
-// Joins the parts of the items that k_kv_rows or k_kv_tiles split.  Blocks (i, .) take
-// the item that begins in worker i's share there and goes on into the next ones.  With
-// few parts every row gets a warp; with many, block (i, y) takes rows y, y + gridDim.y,
-// .. and its warps take every kJoinWarps-th part.  The weights of all parts come first
-// (one load a lane), so the parts' loads do not wait for one another.  All sums have a
-// fixed order.  About 5 us behind a call that cuts few items, 9 us behind 1,776 shares.
+// Joins the parts of the items that k_kv_rows or k_kv_tiles split: an item that begins in
+// worker i's share and goes on into the next ones.  A block (x, .) looks after
+// kJoinHeads workers.  Items of few parts are joined a row to a warp; those of many a row
+// to a block (the y-th block of x takes rows y, y + gridDim.y, ..), whose warps take every
+// kJoinWarps-th part.  The weights of all parts come first (one load a lane), so the
+// parts' loads do not wait for one another.  All sums have a fixed order.
 constexpr int kJoinWarps = 8, kFewParts = 32, kMostParts = 2368;
+template <int R>
+__host__ __device__ constexpr int join_heads() { return R > 16 ? 1 : 4; }
+
 template <int D, typename T, int R>
-__global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a) {
+struct Join {
+  static constexpr int kPer = D / 32, kRound = 4;
+  static constexpr int64_t kPart = (int64_t)R * (D + 2);
+  const AttendArgs& a;
+  PartHead head;
+  const float* all;  // of the worker that begins the item
+  int parts, row, lane;
+
+  __device__ __forceinline__ Join(const AttendArgs& args, int first, const PartHead& h)
+      : a(args), head(h), all(args.parts + (int64_t)first * 2 * kPart), parts(h.last - first + 1),
+        row(0), lane(threadIdx.x & 31) {}
+  // part i: the first one is what its worker began, the others what theirs go on with
+  __device__ __forceinline__ const float* part(int i) const {
+    return all + (i ? (int64_t)i * 2 : 1) * kPart;
+  }
+  __device__ __forceinline__ float2 ml(int i) const {
+    return *reinterpret_cast<const float2*>(part(i) + R * D + row * 2);
+  }
+  // weight of a part; a part without a key has l = 0, one of NaN alone m = -inf
+  __device__ __forceinline__ static float weight(float2 x, float M) {
+    return x.y == 0.f ? 0.f : x.x == -CUDART_INF_F ? 1.f : exp2_fast(x.x - M);
+  }
+  __device__ __forceinline__ bool real(const Request& req) const {
+    return head.tile * R + row < req.w * a.G;
+  }
+  // parts from, from + step, ..; weights by w(i)
+  template <typename W>
+  __device__ __forceinline__ void add(int from, int step, W w, float (&o)[kPer]) const {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) o[k] = 0.f;
+    for (int i0 = from; i0 < parts; i0 += step * kRound) {
+      float x[kRound][kPer], e[kRound];
+#pragma unroll
+      for (int j = 0; j < kRound; ++j) {
+        const int i = i0 + j * step;
+        e[j] = w(i);  // (the whole warp: it may be a shuffle)
+        if (i < parts) {
+          const float* p = part(i) + row * D + lane;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) x[j][k] = p[32 * k];
+        } else {
+          e[j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kRound; ++j)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (e[j] != 0.f) o[k] = __fmaf_rn(x[j][k], e[j], o[k]);
+    }
+  }
+  __device__ __forceinline__ void store(const Request& req, const float (&o)[kPer], float M,
+                                        float L) const {
+    const int at = head.tile * R + row, t = at / a.G;
+    const int hq = head.h * a.G + at - t * a.G;
+    T* out = static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      out[lane + 32 * k] = (T)(L == 0.f ? 0.f : __fdiv_rn(o[k], L));
+    if (a.lse && lane == 0)
+      a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
+          L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
+  }
+};
+
+template <int D, typename T, int R>
+__global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a, int workers) {
   pdl_enter();
-  const PartHead head = a.heads[blockIdx.x];
-  if (head.last < 0) return;
-  const int first = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int parts = head.last - first + 1;
-  const bool few = parts <= kFewParts;
-  const int step = few ? 1 : kJoinWarps, rows_at_once = few ? kJoinWarps * gridDim.y : gridDim.y;
-  int row = few ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
-  if (row >= R) return;
-  const Request req = request_of(a, head.b, false);
+  constexpr int kHeads = join_heads<R>();
   __shared__ float s_w[kMostParts];       // weights of many parts
   __shared__ float s_o[kJoinWarps][D];
   __shared__ float s_r[2][kJoinWarps];
-  constexpr int kPer = D / 32, kRound = 4;
-  constexpr int64_t kPart = (int64_t)R * (D + 2);
-  const float* all = a.parts + (int64_t)first * 2 * kPart;
-  // part i: the first one is what its worker began, the others what theirs go on with
-  auto part = [&](int i) { return all + (i ? (int64_t)i * 2 : 1) * kPart; };
-  // weight of a part; a part without a key has l = 0, one of NaN alone m = -inf
-  auto weight = [&](float2 ml, float M) {
-    return ml.y == 0.f ? 0.f : ml.x == -CUDART_INF_F ? 1.f : exp2_fast(ml.x - M);
-  };
-  for (; row < R; row += rows_at_once) {
-    const int at = head.tile * R + row;
-    if (at >= req.w * a.G) return;
-    auto ml_of = [&](int i) { return *reinterpret_cast<const float2*>(part(i) + R * D + row * 2); };
-    float M = -CUDART_INF_F, L = 0.f, mine = 0.f;
-    if (few) {
-      const float2 ml = lane < parts ? ml_of(lane) : make_float2(-CUDART_INF_F, 0.f);
-      M = ml.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first0 = blockIdx.x * kHeads;
+  for (int task = blockIdx.y * kJoinWarps + warp; task < kHeads * R; task += gridDim.y * kJoinWarps) {
+    const int first = first0 + task / R;
+    if (first >= workers) break;
+    const PartHead head = a.heads[first];
+    if (head.last < 0 || head.last - first >= kFewParts) continue;
+    Join<D, T, R> join(a, first, head);
+    join.row = task % R;
+    const Request req = request_of(a, head.b, false);
+    if (!join.real(req)) continue;
+    const float2 ml = lane < join.parts ? join.ml(lane) : make_float2(-CUDART_INF_F, 0.f);
+    float M = ml.x;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
-      mine = weight(ml, M);
-      L = ml.y == 0.f ? 0.f : __fmul_rn(ml.y, mine);
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
+    const float mine = join.weight(ml, M);
+    float L = ml.y == 0.f ? 0.f : __fmul_rn(ml.y, mine);
 #pragma unroll
-      for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
-    } else {
-      for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) {
-        s_w[i] = ml_of(i).x;
+    for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
+    float o[D / 32];
+    join.add(0, 1, [&](int i) { return __shfl_sync(kAll, mine, i & 31); }, o);
+    join.store(req, o, M, L);
+  }
+  for (int n = 0; n < kHeads; ++n) {
+    const int first = first0 + n;
+    if (first >= workers) break;
+    const PartHead head = a.heads[first];
+    if (head.last < 0 || head.last - first < kFewParts) continue;
+    Join<D, T, R> join(a, first, head);
+    const Request req = request_of(a, head.b, false);
+    for (join.row = blockIdx.y; join.row < R && join.real(req); join.row += gridDim.y) {
+      float M = -CUDART_INF_F, L = 0.f;
+      for (int i = threadIdx.x; i < join.parts; i += 32 * kJoinWarps) {
+        s_w[i] = join.ml(i).x;
         M = fmaxf(M, s_w[i]);
       }
 #pragma unroll
@@ -747,8 +815,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a) {
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_r[0][w]);
-      for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) {
-        const float l = ml_of(i).y, e = weight(make_float2(s_w[i], l), M);
+      for (int i = threadIdx.x; i < join.parts; i += 32 * kJoinWarps) {
+        const float l = join.ml(i).y, e = join.weight(make_float2(s_w[i], l), M);
         s_w[i] = e;
         if (l != 0.f) L = __fmaf_rn(l, e, L);
       }
@@ -759,51 +827,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a) {
       L = 0.f;
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) L = __fadd_rn(L, s_r[1][w]);
-    }
-    float o[kPer];
+      float o[D / 32];
+      join.add(warp, kJoinWarps, [&](int i) { return i < join.parts ? s_w[i] : 0.f; }, o);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) o[k] = 0.f;
-    for (int i0 = few ? 0 : warp; i0 < parts; i0 += step * kRound) {
-      float x[kRound][kPer], e[kRound];
-#pragma unroll
-      for (int j = 0; j < kRound; ++j) {
-        const int i = i0 + j * step;
-        e[j] = few ? __shfl_sync(kAll, mine, i & 31) : i < parts ? s_w[i] : 0.f;
-        if (i >= parts) e[j] = 0.f;
-        if (i < parts) {
-          const float* p = part(i) + row * D + lane;
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) x[j][k] = p[32 * k];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kRound; ++j)
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (e[j] != 0.f) o[k] = __fmaf_rn(x[j][k], e[j], o[k]);
-    }
-    if (!few) {
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) s_o[warp][lane + 32 * k] = o[k];
+      for (int k = 0; k < D / 32; ++k) s_o[warp][lane + 32 * k] = o[k];
       __syncthreads();
       if (warp == 0) {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
+        for (int k = 0; k < D / 32; ++k)
 #pragma unroll
           for (int w = 1; w < kJoinWarps; ++w) o[k] = __fadd_rn(o[k], s_o[w][lane + 32 * k]);
+        join.store(req, o, M, L);
       }
       __syncthreads();  // the arrays are free for the next row
-      if (warp) continue;
     }
-    const int t = at / a.G;
-    const int hq = head.h * a.G + at - t * a.G;
-    T* out = static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      out[lane + 32 * k] = (T)(L == 0.f ? 0.f : __fdiv_rn(o[k], L));
-    if (a.lse && lane == 0)
-      a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
-          L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
   }
 }
 

@@ -286,7 +286,7 @@ struct TileWalk {
 // What the other warps need of an item; steps == 0 ends the list.
 struct TileItem {
   int b, h, tile, start, w, L;
-  int key0, hi;        // first key of the share's steps; one behind the last key seen
+  int key0;            // first key of the share's steps
   int steps;
   int whole;           // bit 0: the share holds the item's first step, bit 1: its last
   int last;            // block whose share ends the item
@@ -866,7 +866,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           x->w = walk.req.w;
           x->L = walk.req.L;
           x->key0 = walk.range.lo + walk.s0 * kTileKeys;
-          x->hi = walk.range.hi;
           x->whole = (walk.begins() ? 1 : 0) | (walk.ends() ? 2 : 0);
           x->last = walk.last_block(per);
         }

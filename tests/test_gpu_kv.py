@@ -386,12 +386,25 @@ def test_attend_tiles_of_many_requests(kv, kind):
     rng = np.random.default_rng(33)
     n = 1500
     new = rng.integers(0, 4, n)
-    new[::97] = rng.integers(20, 150, len(new[::97]))
+    new[::97] = rng.integers(20, 150, len(new[::97]))  # more rows than the row kernel takes
     lens = rng.integers(0, 60, n)
     lens[::50] += 300
     c = history(33, lens, new, 4, 2, 64, 16, kind)
     run_attend(kv, c)
     run_attend(kv, c, causal=False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,new,D", [(63, 4, 128), (64, 4, 128), (64, 5, 128), (64, 8, 64), (64, 9, 64),
+                                     (300, 3, 64)])
+def test_attend_between_the_row_and_the_tile_kernel(kv, kind, n, new, D):
+    """8 query heads a kv head: 24 to 72 rows, fewer and more requests."""
+    rng = np.random.default_rng(37)
+    w = rng.integers(0, new + 1, n)
+    w[3] = new
+    c = history(37, rng.integers(0, 400, n) + w, w, 8, 1, D, 16, kind)
+    run_attend(kv, c)
+    run_attend(kv, c, window=100)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
