@@ -379,7 +379,7 @@ constexpr uint32_t kOffPlus2 = 0xE480E480u, kOffMinus2 = 0x64806480u;  // -1152,
 // of 6,000 in all; the tensor pipe is busy 0.30 of the time.  Six chunks of 500 to 4,096
 // rows behind up to 8,000 keys, 16 query and 4 kv heads x 128, bf16 (133 GFLOP): 227 us,
 // 585 TFLOP/s, 0.36 of the measured matrix rate; 32 x 1,024 candidates, 8 heads x 64, fp16
-// (72 GFLOP): 223 us.  What it went through: one thread a row with 128 keys 660 us; bulk
+// (72 GFLOP): 253 us (222 before the weights' second part).  What it went through: one thread a row with 128 keys 660 us; bulk
 // copies and smaller code (the roles together overran the instruction cache) 513;
 // queries copied under the last step 373; two threads a row 283; item cost in the shares
 // 250; products issued from warp-uniform code 233.  Scales: the score factor holds the key scale (one for 16
@@ -396,6 +396,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
   pdl_trigger();
   using L = TileSmem<D>;
   constexpr bool kBf16 = __is_same(T, __nv_bfloat16);  // queries and keys go as they are
+  // fp16 results get the weights in two fp16 parts: with one they were 1.4 to 1.5 times as
+  // far from 64 bits as their own rounding (3.0e-4 against 2.1e-4); bf16's hides it.
+  constexpr bool kTwo = !kBf16;
   extern __shared__ __align__(16) uint8_t s_tile[];
   const uint32_t base = (smem_addr(s_tile) + 1023) & ~1023u;
   TileSmall* sm = reinterpret_cast<TileSmall*>(s_tile + (base - smem_addr(s_tile)) + L::kSmall);
@@ -663,6 +666,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         // before it is taken off; below, one fma does.
         const float top = m == -CUDART_INF_F ? 0.f : m;
         const bool big = __any_sync(kAll, fabsf(top) > 1048576.f);
+        uint32_t low[16];  // kTwo: second parts, which wait until their place has been read
 #pragma unroll 1
         for (int cnk = 0; cnk < 2; ++cnk) {
           uint32_t y[32];
@@ -678,6 +682,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             lp[g] = x < -60.f ? -60.f : x;
           }
           tmem_loaded(y);
+          if (kTwo && cnk == 1) tmem_store16(t_s + 32, low);
           if (big) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -711,9 +716,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           }
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = half2_bits(p[2 * e], p[2 * e + 1]);
+          for (int e = 0; e < 16; ++e) {
+            pk[e] = half2_bits(p[2 * e], p[2 * e + 1]);
+            if constexpr (kTwo) {
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&pk[e]));
+              low[e] = half2_bits(__fsub_rn(p[2 * e], h.x), __fsub_rn(p[2 * e + 1], h.y));
+            }
+          }
           tmem_store16(t_s + cnk * 16, pk);
         }
+        if (kTwo) tmem_store16(t_s + 48, low);
         tmem_stored();
         tc_fence_before();
         bar_arrive(&sm->p_full[half]);
@@ -1000,6 +1012,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             for (int kk = 0; kk < kTileKeys / 16; ++kk)
               mma_ts(leader, d, p + (kk / 4) * 64 + (kk % 4) * 8, v + kk * (2048 >> 4), kHigh, kOut,
                      kk > 0 || j > 0);
+            if constexpr (kTwo) {
+#pragma unroll
+              for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                mma_ts(leader, d, p + (kk / 4) * 64 + 32 + (kk % 4) * 8, v + kk * (2048 >> 4), kHigh,
+                       kOut, true);
+            }
             if (i == halves - 1) tc_commit(leader, &sm->free[1][stage]);
             if (j == n_steps - 1) {
               tc_commit(leader, &sm->o_full[i]);

@@ -147,8 +147,6 @@ def attend_bound(out, size, keys, D, kind):
     spread, reach, codes = size
     chain = keys / (16 if kind == "fp32" else 4) + 32
     weight = 2.0**-11 if kind == "bf16" else 2.0**-22
-    if kind == "fp16":
-        weight = 2.0**-11  # the tile kernel keeps one part for both 16-bit types
     off = 2 * ((D + 10) * 2.0**-23 * reach[..., None] + 2.0**-21 + chain * 2.0**-23) + weight
     half = {"bf16": 2.0**-8, "fp16": 2.0**-11, "fp32": 2.0**-24}[kind]
     tiny = {"bf16": 0.0, "fp16": 2.0**-25, "fp32": 0.0}[kind]
