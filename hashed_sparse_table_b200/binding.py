@@ -526,8 +526,8 @@ def _kv_rows(device: int, t, name: str, n: int, heads: int, dim: int, dtype):
     """Element strides (row, head) of [n, heads, dim] with contiguous values of a head."""
     if t.shape == (n, heads, dim) and t.dtype is dtype and t.get_device() == device:
         sn, sh, sd = t.stride()
-        if sd == 1:
-            return sn, sh
+        if sd == 1:  # (a dimension of one has any stride)
+            return (sn if n > 1 else 0), (sh if heads > 1 else 0)
     raise ValueError(f"{name}: expected [{n}, {heads}, {dim}] of {dtype} on cuda:{device}, the "
                      f"current device, with contiguous heads, got {t.dtype} {tuple(t.shape)} with "
                      f"strides {t.stride()} on {t.device}")

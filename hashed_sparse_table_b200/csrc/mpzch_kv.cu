@@ -254,6 +254,8 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
       !rows_ok(q, q_stride_n, q_stride_h, bytes) || !rows_ok(out, out_stride_n, out_stride_h, bytes) ||
       !aligned16(k_cache) || !aligned16(v_cache))
     return MPZCH_EINVAL;
+  // heads of the output must not lie on one another
+  if ((n > 1 && out_stride_n < dim) || (q_heads > 1 && out_stride_h < dim)) return MPZCH_EINVAL;
   AttendArgs a;
   a.q = q;
   a.qsn = q_stride_n;

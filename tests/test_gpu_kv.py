@@ -472,6 +472,18 @@ def test_attend_strides_untouched_rows_and_scales(kv, kind):
     run_attend(kv, c, q=wide[:, 2:6], out=out[:, 3:7].fill_(7.0), scale=0.0, causal=False)
 
 
+@pytest.mark.parametrize("rows,Hq", [(1, 2), (3, 1), (1, 1), (25, 1)])
+def test_attend_dimensions_of_one_with_any_stride(kv, rows, Hq):
+    """One row, one head: torch gives such a dimension whatever stride the view came with."""
+    c = history(38, [90], [rows], Hq, 1, 64, 16, "bf16")
+    shape, full = (rows, Hq, 64), c["q"].stride()
+    stride = (full[0] if rows > 1 else 77, full[1] if Hq > 1 else 33, 1)
+    q = torch.as_strided(c["q"].cuda(), shape, stride)
+    out = torch.as_strided(torch.full((rows * Hq * 64,), 7.0, dtype=torch.bfloat16, device="cuda"),
+                           shape, stride)
+    run_attend(kv, c, q=q, out=out)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("rows", [1, 40])
 def test_attend_value_scales_far_apart(kv, kind, rows):

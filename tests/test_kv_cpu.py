@@ -74,7 +74,7 @@ def attend(lib, **change):
     dict(scale=float("nan")), dict(scale=3e38), dict(n=2**31 // 4), dict(window=-1), dict(window=4, causal=0), dict(q=None),
     dict(out=None), dict(cu=None), dict(seq=None), dict(table=None), dict(kc=None), dict(vc=None),
     dict(ks=None), dict(vs=None), dict(ws=None), dict(ws_bytes=100), dict(ws=FAKE + 16),
-    dict(q=FAKE + 4), dict(out=FAKE + 8), dict(qsn=250), dict(osh=-64), dict(kc=FAKE + 1)])
+    dict(q=FAKE + 4), dict(out=FAKE + 8), dict(osn=0), dict(osh=0), dict(osh=32), dict(osn=56), dict(qsn=250), dict(osh=-64), dict(kc=FAKE + 1)])
 def test_attend_refusals(lib, change):
     assert attend(lib, **change) == EINVAL
 
