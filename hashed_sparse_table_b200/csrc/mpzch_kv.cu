@@ -89,10 +89,14 @@ int launch_tiles(const AttendArgs& a, cudaStream_t st) {
   return rc;
 }
 
-// Histories up to this long go whole to a warp each: its 32 steps take about as long as
-// the launch that would join the parts of a cut one (4 requests x 8 heads of up to 300
-// keys, dim 64, on the device: one launch 11.5 us, cut and joined 8.5 + 5.1 us; and a
-// caller issues one launch fewer, 16.6 against 18.5 us a call).
+// Histories up to kWholeKeys of few items (request, kv head) go whole to a warp each: its
+// 32 steps take about as long as the launch that would join the parts of cut ones (4
+// requests x 8 heads of up to 300 keys, dim 64, on the device: one launch 11.5 us, cut and
+// joined 8.5 + 5.1 us; and a caller issues one launch fewer, 16.6 against 18.5 us a call).
+// Many items balance better cut (128 x 8 of up to 500 keys 17 us, whole 22; 366 x 8 of up to
+// 271 keys 26 : 31), unless they are a step or two long (1,749 x 8 of up to 3 keys, 8 query
+// heads each: 33 us, whole 30).
+constexpr int64_t kTinyKeys = 128, kWholeItems = 256;
 constexpr int64_t kWholeKeys = 512;
 
 template <int D, typename T, int R, int NQ, int NP>
@@ -285,7 +289,10 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
                   out_stride_h * bytes % 32 == 0;
   a.lse = lse;
   a.status = dev_status;
-  a.unit_keys = (int64_t)max_blocks * block_size <= kWholeKeys ? 1 << 30 : kUnitKeys;
+  const int64_t most = (int64_t)max_blocks * block_size;
+  a.unit_keys = most <= kTinyKeys || (most <= kWholeKeys && (int64_t)a.B * a.H <= kWholeItems)
+                    ? 1 << 30
+                    : kUnitKeys;
   a.item_cost = a.unit_keys == kUnitKeys ? kRowItemCost : 0;
   a.max_new = max_new;
   a.heads = static_cast<PartHead*>(workspace);

@@ -444,12 +444,15 @@ def test_attend_tiles_scores_far_apart(kv, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("length", [496, 512, 513, 528])
-def test_attend_around_the_longest_whole_history(kv, kind, length):
-    """Tables that hold up to 512 keys and more: items go whole to a warp, or are cut."""
-    c = history(36, [length, 40, 0, length - 7], [1, 2, 1, 1], 4, 2, 64, 16, kind)
+@pytest.mark.parametrize("length", [112, 128, 129, 144, 496, 512, 513, 528])
+@pytest.mark.parametrize("more", [0, 124, 125])
+def test_attend_around_the_longest_whole_history(kv, kind, length, more):
+    """Tables that hold up to 128 or 512 keys and more, of up to 256 items and more: items go
+    whole to a warp, or are cut."""
+    c = history(36, [length, 40, 0, length - 7] + [9] * more, [1, 2, 1, 1] + [1] * more, 4, 2, 64, 16,
+                kind)
     for width in (length // 16 + 1, length // 16 + 40):
-        t = np.full((4, width), -1, np.int32)
+        t = np.full((4 + more, width), -1, np.int32)
         t[:, :min(width, c["table"].shape[1])] = c["table"][:, :width]
         run_attend(kv, {**c, "table": t})
 
