@@ -206,8 +206,10 @@ __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
 // most 2^kSlack (the maximum is moved only when a score passes it by more than
 // that), so the largest is 2^15; weights below 2^-21 of the largest lose bits and
 // those below 2^-32 vanish.
+// vref is 2^-119 at least, so that 2^7 / vref is finite: below it weights lose bits early.
 constexpr float kSlack = 8.f;
 constexpr float kWeightScale = 128.f;
+constexpr int kLeastRef = 127 - 119;  // exponent field
 
 // 16-key slots of a warp's ring: one being read, the others in flight.  12 KB a warp
 // at D = 128: 12 warps of an SM have 96 KB under way.  (256 single tokens x 8 heads x
@@ -565,8 +567,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
       if (__any_sync(kAll, up || vup)) {
         float beta = 1.f;
         if (vup) {  // the next power of two, twice the largest scale at most
-          const uint32_t e = (__float_as_uint(va) >> 23) + 1;
-          const float to = __uint_as_float((e > 254 ? 254 : e) << 23);
+          const int e = (int)(__float_as_uint(va) >> 23) + 1;
+          const float to = __int_as_float(max(kLeastRef, min(254, e)) << 23);
           beta = __fdiv_rn(vref, to);
           vref = to;
           weight = __fdiv_rn(kWeightScale, vref);
@@ -661,13 +663,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
         L += __shfl_xor_sync(kAll, L, 8);
         L += __shfl_xor_sync(kAll, L, 16);
         if (row >= n_rows) continue;
-        // a row that saw no key has an all-zero accumulator
-        const float g = whole ? (L == 0.f ? 0.f : __fdiv_rn(unit, L)) : unit;
+        // a row that saw no key has an all-zero accumulator; unit / L, but for its underflow
+        const float g = whole ? (L == 0.f ? 0.f : __fdiv_rn(1.f, L)) : 1.f;
         const int at = first_row + row, t = at / a.G;
         const int hq = h * a.G + at - t * a.G;
         float o[D / 8];
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) o[k] = __fmul_rn(acc[i][k / 2][2 * (k & 1) + j], g);
+        for (int k = 0; k < D / 8; ++k) o[k] = __fmul_rn(__fmul_rn(acc[i][k / 2][2 * (k & 1) + j], g), unit);
         const int d = r * (D / 8);
         if (whole) {
           store_row<T>(static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh + d, o);

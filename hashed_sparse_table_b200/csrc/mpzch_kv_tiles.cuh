@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       tc_fence_after();
       const int hq = item.h * a.G + (real ? row - t * a.G : 0);
       const float unit = __fmul_rn(vref, 1.f / kWeightScale);
-      const float g = whole ? __fdiv_rn(unit, sum) : unit;
+      const float g = whole ? __fdiv_rn(1.f, sum) : 1.f;  // unit / sum, but for its underflow
       const int prow = half * 128 + at_row;
       float* out_part = a.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kTileRows * (D + 2) +
                         prow * D + part * (D / 2);
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           // a row that saw no key: 0, whatever the hidden blocks hold
-          x[e] = sum == 0.f ? 0u : __float_as_uint(__fmul_rn(__uint_as_float(x[e]), g));
+          x[e] = sum == 0.f ? 0u : __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(x[e]), g), unit));
         if (!real) continue;
         if (whole) {
           uint32_t y[16];

@@ -1,0 +1,58 @@
+"""History cache on the GPU at the ends of its number ranges: value scales near the smallest
+numbers of binary32."""
+import numpy as np
+import pytest
+import torch
+
+import kv_ref as ref
+from test_gpu_kv import dev, history, kv  # noqa: F401 (kv: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(kv, c, causal=False, window=0, scale=0.125):
+    """(out, want, size) for the case, rows of no request not expected."""
+    q = c["q"].cuda()
+    out = torch.full_like(q, 7.0)
+    kv.mpzch_kv_attend(q, *(dev(c[x]) for x in ("kc", "vc", "ks", "vs", "table", "cu", "seq")),
+                       int(np.diff(c["cu"]).max()), out, softmax_scale=scale, causal=causal,
+                       window=window)
+    want, _, size = ref.attend(c["q"].double().numpy(), c["kc"], c["vc"], c["ks"], c["vs"],
+                               c["table"], c["cu"], c["seq"], scale, causal, window)
+    return out.double().cpu().numpy(), want, size
+
+
+def bound(want, size, keys, D, kind, low=None):
+    """ref.attend_bound without its absolute allowance: `low` (the same as size[2], for the weights
+    that are subnormal in fp16) if given, what the smallest reference of the weights, 2^-119,
+    leaves (2^-25 2^-7 2^-118 for each code), and half a step of the smallest numbers of the type
+    and of binary32 (two roundings there)."""
+    spread, reach, codes = size
+    half = {"bf16": 2.0**-8, "fp16": 2.0**-11, "fp32": 2.0**-24}[kind]
+    tiny = {"bf16": 2.0**-134, "fp16": 2.0**-25, "fp32": 0.0}[kind] + 2.0**-149
+    full = ref.attend_bound(want, (spread, reach, codes if low is None else low), keys, D, kind)
+    full -= 1e-37 + (2.0**-25 if kind == "fp16" else 0.0)
+    return full + tiny + keys * 127 * 2.0**-150 * (1 + half)
+
+
+# ------------------------------------------------------------------ attention: smallest scales
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("size", [2.0**-121, 2.0**-122, 1e-40, 1e-44])
+@pytest.mark.parametrize("length", [100, 3000])
+def test_attend_smallest_value_scales(kv, kind, rows, size, length):
+    """Every block of one request next to nothing; of the next one the first blocks alone, in
+    front of ordinary ones; of the third every other."""
+    c = history(50, [length] * 3, [rows] * 3, 2, 2, 64, 16, kind)
+    n = -(-length // 16)
+    small = np.float32(size) * (1 + np.arange(n) % 3).astype(np.float32)[:, None]
+    c["vs"][c["table"][0, :n]] = small
+    c["vs"][c["table"][1, :3]] = small[:3]
+    c["vs"][c["table"][2, :n:2]] = small[::2]
+    got, want, s = attend(kv, c)
+    assert np.isfinite(got).all()
+    for b in range(3):
+        at = slice(b * rows, b * rows + rows)
+        mine = tuple(x[at] for x in s)
+        assert (np.abs(got - want)[at] <= bound(want[at], mine, length, 64, kind)).all(), b
+    assert kind == "fp16" or size < 1e-40 or (got[:rows] != 0).any()
