@@ -308,10 +308,14 @@ __device__ __forceinline__ float absmax_value(uint32_t a) {
 // reciprocal rcp is the correctly rounded quotient when q is within an ulp of it, which
 // the first correction sees to (x rcp is within 1.5).  That needs s in the middle of the
 // exponent range; elsewhere (uniformly for a run) the values are divided.  The integer
-// then comes out of adding 1.5 2^23, in the low byte of the sum.
-__device__ __forceinline__ uint4 codes16(const uint64_t (&x)[8], float s, float rcp) {
+// then comes out of adding 1.5 2^23, in the low byte of the sum.  A run's own values give
+// quotients of 127 at most; held ones (kCut; `near`: the old scale is within 2^20 s) pass
+// it where the old scale is negative or a code is -128, neither of which an append leaves.
+template <bool kCut>
+__device__ __forceinline__ uint4 codes16(const uint64_t (&x)[8], float s, float rcp, bool near) {
   uint32_t b[16];
-  if (s >= 0x1p-80f && s <= 0x1p100f) {
+  auto cut = [](float q) { return fminf(fmaxf(q, -127.f), 127.f); };
+  if (s >= 0x1p-80f && s <= 0x1p100f && near) {
     const uint64_t r2 = pair(rcp, rcp), s2 = pair(-s, -s), magic = pair(kRoundMagic, kRoundMagic);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -319,6 +323,10 @@ __device__ __forceinline__ uint4 codes16(const uint64_t (&x)[8], float s, float 
       q = fma2(fma2(q, s2, x[i]), r2, q);
       q = fma2(fma2(q, s2, x[i]), r2, q);
       float lo, hi;
+      if constexpr (kCut) {
+        unpair(q, lo, hi);
+        q = pair(cut(lo), cut(hi));
+      }
       unpair(add2(q, magic), lo, hi);
       b[2 * i] = __float_as_uint(lo);
       b[2 * i + 1] = __float_as_uint(hi);
@@ -328,8 +336,8 @@ __device__ __forceinline__ uint4 codes16(const uint64_t (&x)[8], float s, float 
     for (int i = 0; i < 8; ++i) {
       float lo, hi;
       unpair(x[i], lo, hi);
-      b[2 * i] = max(-127, min(127, rne_small(__fdiv_rn(lo, s))));
-      b[2 * i + 1] = max(-127, min(127, rne_small(__fdiv_rn(hi, s))));
+      b[2 * i] = rne_small(cut(__fdiv_rn(lo, s)));
+      b[2 * i + 1] = rne_small(cut(__fdiv_rn(hi, s)));
     }
   }
   return make_uint4(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]),
@@ -440,7 +448,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) k_kv_append(Appen
           for (int j = 0; j < 8; ++j)
             y[j] = pair(__fmul_rn((float)(int8_t)(w[j / 2] >> (16 * (j % 2))), before),
                         __fmul_rn((float)(int8_t)(w[j / 2] >> (16 * (j % 2) + 8)), before));
-          *c = usable ? codes16(y, s, rcp) : make_uint4(0, 0, 0, 0);
+          *c = usable ? codes16<true>(y, s, rcp, fabsf(before) <= __fmul_rn(s, 0x1p20f))
+                      : make_uint4(0, 0, 0, 0);
         }
       }
 #pragma unroll
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) k_kv_append(Appen
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[j] = raw_pair(x[i], j);
           *reinterpret_cast<uint4*>(base + (int64_t)(o + i * kTok + tok) * D) =
-              usable ? codes16(y, s, rcp) : make_uint4(0, 0, 0, 0);
+              usable ? codes16<false>(y, s, rcp, true) : make_uint4(0, 0, 0, 0);
         }
       __syncwarp();  // every lane has read the old scale (W > 1: and every warp)
       if (wi == 0 && lane == 0) *sp = s;

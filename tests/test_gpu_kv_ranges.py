@@ -1,11 +1,11 @@
 """History cache on the GPU at the ends of its number ranges: value scales near the smallest
-numbers of binary32."""
+numbers of binary32, and held codes under negative scales."""
 import numpy as np
 import pytest
 import torch
 
 import kv_ref as ref
-from test_gpu_kv import dev, history, kv  # noqa: F401 (kv: fixture)
+from test_gpu_kv import dev, history, kv, make_cache, run_append  # noqa: F401 (kv: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,30 @@ def test_attend_smallest_value_scales(kv, kind, rows, size, length):
         mine = tuple(x[at] for x in s)
         assert (np.abs(got - want)[at] <= bound(want[at], mine, length, 64, kind)).all(), b
     assert kind == "fp16" or size < 1e-40 or (got[:rows] != 0).any()
+
+
+# ------------------------------------------------------------------ append: held codes
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("D,bs", [(32, 16), (128, 128)])
+def test_append_behind_negative_scales_and_lowest_codes(kv, kind, D, bs):
+    """Held codes whose quotient passes 127: the old scale is negative and larger than the new one
+    (by little, by much, beyond the range of the packed quotient), or the code is -128."""
+    rng = np.random.default_rng(51)
+    H, blocks = 2, 24
+    kc, ks = make_cache(rng, blocks, H, bs, D)
+    vc, vs = make_cache(rng, blocks, H, bs, D)
+    for cache in (kc, vc):
+        cache[:, :, ::3] = -128
+        cache[:, :, 1::5, 3] = 100
+    size = np.float32(10.0) ** rng.uniform(-3, 8, (blocks, H)).astype(np.float32)
+    ks[:12], vs[4:16] = -size[:12], -size[4:16]
+    ks[20], vs[20] = -1e-30, 1e-30
+    ks[21], vs[21] = -3e38, -1e-40
+    slots = np.concatenate([b * bs + np.arange(9, 12) for b in range(blocks)])
+    k, v = (rng.standard_normal((len(slots), H, D)).astype(np.float32) for _ in range(2))
+    at = slice(20 * 3, 22 * 3)
+    if kind != "fp16":
+        k[at] *= np.float32(1e-31)
+        v[at] *= np.float32(1e-31)
+    k[3 * 3:4 * 3], v[5 * 3:6 * 3] = 0, 0  # the new scale is 0
+    run_append(kv, k, v, slots, kc, vc, ks, vs, kind)
