@@ -35,6 +35,19 @@ bool rows_ok(const void* p, int64_t sn, int64_t sh, int bytes) {
          sn < (1ll << 40) && sh < (1ll << 40);
 }
 
+// Whether any two of n x h heads of `dim` elements, sn and sh elements apart, share one.  Where
+// one stride passes all that lies in the other (every ordinary view) that is seen at once;
+// else, for each distance in heads, the two nearest distances in rows are looked at.
+bool heads_overlap(int64_t n, int64_t sn, int64_t h, int64_t sh, int64_t dim) {
+  if ((n > 1 && sn < dim) || (h > 1 && sh < dim)) return true;
+  if (n <= 1 || h <= 1 || sn >= (h - 1) * sh + dim || sh >= (n - 1) * sn + dim) return false;
+  for (int64_t j = 1; j < h; ++j) {
+    const int64_t i = j * sh / sn, off = j * sh - i * sn;  // 0 <= off < sn
+    if ((i < n && off < dim) || (i + 1 < n && sn - off < dim)) return true;
+  }
+  return false;
+}
+
 template <typename T, int D, int W>
 int launch_append(const AppendArgs& a, cudaStream_t st) {
   const void* kern = reinterpret_cast<const void*>(k_kv_append<T, D, W>);
@@ -258,8 +271,7 @@ int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64
       !rows_ok(q, q_stride_n, q_stride_h, bytes) || !rows_ok(out, out_stride_n, out_stride_h, bytes) ||
       !aligned16(k_cache) || !aligned16(v_cache))
     return MPZCH_EINVAL;
-  // heads of the output must not lie on one another
-  if ((n > 1 && out_stride_n < dim) || (q_heads > 1 && out_stride_h < dim)) return MPZCH_EINVAL;
+  if (heads_overlap(n, out_stride_n, q_heads, out_stride_h, dim)) return MPZCH_EINVAL;
   AttendArgs a;
   a.q = q;
   a.qsn = q_stride_n;

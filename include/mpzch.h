@@ -339,7 +339,8 @@ MPZCH_API int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, i
  * k_j, v_j the values (code * scale) of kv head h / (q_heads / kv_heads).  A row
  * that sees no key gives out = 0, lse = -inf.  lse: nullable device fp32
  * [n][q_heads], natural logarithm of the softmax's denominator.  q, out: device
- * [n][q_heads][dim] of type dtype, strides in elements as for mpzch_kv_append.
+ * [n][q_heads][dim] of type dtype, strides in elements as for mpzch_kv_append; strides
+ * that lay one head of out on another are refused (MPZCH_EINVAL).
  * Rows from cu_new[B] on are neither read nor written.  max_new: the caller's
  * bound on a request's rows; it chooses kernels and changes no result beyond
  * rounding.  n * q_heads and max_blocks * block_size stay below 2^31 - 1024.

@@ -1,0 +1,27 @@
+"""Calls of the history cache that are refused before anything is launched: what the C entries and
+the binding check without a GPU."""
+import itertools
+
+import numpy as np
+import pytest
+
+from test_kv_cpu import EINVAL, attend, lib  # noqa: F401 (lib: fixture)
+
+
+def overlapping(n, sn, h, sh, dim):
+    seen = np.zeros((n - 1) * sn + (h - 1) * sh + dim, int)
+    for i, j in itertools.product(range(n), range(h)):
+        seen[i * sn + j * sh:i * sn + j * sh + dim] += 1
+    return seen.max() > 1
+
+
+@pytest.mark.parametrize("n,H", [(2, 2), (3, 4), (4, 4), (5, 2), (7, 6), (9, 3)])
+def test_outputs_whose_heads_overlap_are_refused(lib, n, H):
+    """Every pair of strides that puts a head on another one, found by counting; 32 elements a
+    head, 8 to a 16-byte boundary."""
+    pairs = [x for x in itertools.product(range(0, 32 * 12 + 1, 8), repeat=2)
+             if overlapping(n, x[0], H, x[1], 32)]
+    for sn, sh in pairs:
+        assert attend(lib, n=n, Hq=H, H=1, D=32, osn=sn, osh=sh) == EINVAL, (sn, sh)
+    # not a matter of each stride alone
+    assert (32, 32) in pairs and (40, 40) in pairs
