@@ -34,7 +34,7 @@ struct AttendArgs {
   int item_cost;      // units that the shares count for an item besides its keys
   int max_new;        // the caller's bound on a request's rows: sizes the join's grid
   struct PartHead* heads;
-  float* parts;       // [warp][2]: [R][D] outputs, [R][2] maxima and sums
+  float* parts;       // [warp][2]: [R][D] means over the part's keys, [R][2] maxima and sums
 };
 
 // What a warp of k_kv_rows leaves for k_kv_join: the item that begins in the
@@ -663,8 +663,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
         L += __shfl_xor_sync(kAll, L, 8);
         L += __shfl_xor_sync(kAll, L, 16);
         if (row >= n_rows) continue;
-        // a row that saw no key has an all-zero accumulator; unit / L, but for its underflow
-        const float g = whole ? (L == 0.f ? 0.f : __fdiv_rn(1.f, L)) : 1.f;
+        // the mean, also of a part (sums of large values would overflow), in two steps, since
+        // unit / L can underflow; a row that saw no key has an all-zero accumulator
+        const float g = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
         const int at = first_row + row, t = at / a.G;
         const int hq = h * a.G + at - t * a.G;
         float o[D / 8];
@@ -722,14 +723,14 @@ struct Join {
   __device__ __forceinline__ float2 ml(int i) const {
     return *reinterpret_cast<const float2*>(part(i) + R * D + row * 2);
   }
-  // weight of a part; a part without a key has l = 0, one of NaN alone m = -inf
-  __device__ __forceinline__ static float weight(float2 x, float M) {
-    return x.y == 0.f ? 0.f : x.x == -CUDART_INF_F ? 1.f : exp2_fast(x.x - M);
+  // a part's share of the sum; a part without a key has l = 0, one of NaN alone m = -inf
+  __device__ __forceinline__ static float sum_of(float2 x, float M) {
+    return x.y == 0.f ? 0.f : x.x == -CUDART_INF_F ? x.y : __fmul_rn(x.y, exp2_fast(x.x - M));
   }
   __device__ __forceinline__ bool real(const Request& req) const {
     return head.tile * R + row < req.w * a.G;
   }
-  // parts from, from + step, ..; weights by w(i)
+  // parts from, from + step, ..; weights, which add up to 1, by w(i)
   template <typename W>
   __device__ __forceinline__ void add(int from, int step, W w, float (&o)[kPer]) const {
 #pragma unroll
@@ -762,7 +763,7 @@ struct Join {
     T* out = static_cast<T*>(a.out) + (req.start + t) * a.osn + hq * a.osh;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-      out[lane + 32 * k] = (T)(L == 0.f ? 0.f : __fdiv_rn(o[k], L));
+      out[lane + 32 * k] = (T)(L == 0.f ? 0.f : o[k]);
     if (a.lse && lane == 0)
       a.lse[(int64_t)(req.start + t) * a.Hq + hq] =
           L == 0.f ? -CUDART_INF_F : __fmul_rn(M + log2f(L), 0.6931471805599453f);
@@ -790,12 +791,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a, in
     float M = ml.x;
 #pragma unroll
     for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
-    const float mine = join.weight(ml, M);
-    float L = ml.y == 0.f ? 0.f : __fmul_rn(ml.y, mine);
+    const float mine = join.sum_of(ml, M);
+    float L = mine;
 #pragma unroll
     for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
+    const float weight = __fdiv_rn(mine, L);  // (all 0 / 0: not used)
     float o[D / 32];
-    join.add(0, 1, [&](int i) { return __shfl_sync(kAll, mine, i & 31); }, o);
+    join.add(0, 1, [&](int i) { return __shfl_sync(kAll, weight, i & 31); }, o);
     join.store(req, o, M, L);
   }
   for (int n = 0; n < kHeads; ++n) {
@@ -818,9 +820,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a, in
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_r[0][w]);
       for (int i = threadIdx.x; i < join.parts; i += 32 * kJoinWarps) {
-        const float l = join.ml(i).y, e = join.weight(make_float2(s_w[i], l), M);
-        s_w[i] = e;
-        if (l != 0.f) L = __fmaf_rn(l, e, L);
+        s_w[i] = join.sum_of(make_float2(s_w[i], join.ml(i).y), M);
+        L = __fadd_rn(L, s_w[i]);
       }
 #pragma unroll
       for (int d = 16; d; d >>= 1) L = __fadd_rn(L, __shfl_xor_sync(kAll, L, d));
@@ -829,8 +830,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 4) k_kv_join(AttendArgs a, in
       L = 0.f;
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) L = __fadd_rn(L, s_r[1][w]);
+      const float inv = __fdiv_rn(1.f, L);
       float o[D / 32];
-      join.add(warp, kJoinWarps, [&](int i) { return i < join.parts ? s_w[i] : 0.f; }, o);
+      join.add(warp, kJoinWarps,
+               [&](int i) { return i < join.parts ? __fmul_rn(s_w[i], inv) : 0.f; }, o);
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) s_o[warp][lane + 32 * k] = o[k];
       __syncthreads();

@@ -747,7 +747,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       tc_fence_after();
       const int hq = item.h * a.G + (real ? row - t * a.G : 0);
       const float unit = __fmul_rn(vref, 1.f / kWeightScale);
-      const float g = whole ? __fdiv_rn(1.f, sum) : 1.f;  // unit / sum, but for its underflow
+      // the mean, also of a part, in two steps, since unit / sum can underflow
+      const float g = __fdiv_rn(1.f, sum);
       const int prow = half * 128 + at_row;
       float* out_part = a.parts + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kTileRows * (D + 2) +
                         prow * D + part * (D / 2);

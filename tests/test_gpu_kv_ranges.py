@@ -1,5 +1,5 @@
-"""History cache on the GPU at the ends of its number ranges: value scales near the smallest
-numbers of binary32, and held codes under negative scales."""
+"""History cache on the GPU at the ends of its number ranges: value scales near the smallest and
+the largest numbers of binary32, and held codes under negative scales."""
 import numpy as np
 import pytest
 import torch
@@ -83,3 +83,18 @@ def test_append_behind_negative_scales_and_lowest_codes(kv, kind, D, bs):
         v[at] *= np.float32(1e-31)
     k[3 * 3:4 * 3], v[5 * 3:6 * 3] = 0, 0  # the new scale is 0
     run_append(kv, k, v, slots, kc, vc, ks, vs, kind)
+
+
+# ------------------------------------------------------------------ attention: largest values
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("length", [100, 20000])
+def test_attend_largest_values(kv, kind, rows, length):
+    """Values whose sum passes the range of binary32 and whose mean does not."""
+    c = history(52, [length, 60], [rows] * 2, 2, 1, 64, 16, kind)
+    c["vs"][:] = np.float32(2.0**120)
+    c["vc"] = (np.abs(c["vc"].astype(np.int16)) // 2 + 60).astype(np.int8)
+    got, want, s = attend(kv, c)
+    assert np.abs(want).max() > 2.0**126
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= bound(want, s, length, 64, kind)).all()
