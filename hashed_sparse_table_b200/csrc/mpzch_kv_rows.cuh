@@ -202,14 +202,34 @@ __device__ __forceinline__ float row_factor(uint32_t amax_bits) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// The softmax weights are kept as p * 2^7 * (value scale / vref) in fp16: p is at
-// most 2^kSlack (the maximum is moved only when a score passes it by more than
-// that), so the largest is 2^15; weights below 2^-21 of the largest lose bits and
-// those below 2^-32 vanish.
-// vref is 2^-119 at least, so that 2^7 / vref is finite: below it weights lose bits early.
+// The softmax weights are kept as p * value scale * 2^7 / 2^ev in fp16.  A row's ev follows
+// the largest product p * value scale that it has met, as the maximum follows its scores:
+// both move only when a key passes them by more than kSlack, so the largest weight is 2^15;
+// weights below 2^-21 of the row's largest lose bits and those below 2^-32 vanish, whatever
+// the scales of blocks that the row does not look at.  Lower bounds of ev (kLeastRef, and
+// kFar below the largest scale of any block so far) keep 2^7 / 2^ev and its product with a
+// scale finite.
 constexpr float kSlack = 8.f;
-constexpr float kWeightScale = 128.f;
-constexpr int kLeastRef = 127 - 119;  // exponent field
+constexpr float kLeastRef = -119.f, kMostRef = 128.f, kFar = 100.f;
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^e, e a whole number from -126 to 127.
+__device__ __forceinline__ float exp2_whole(float e) {
+  return __int_as_float(((int)e + 127) << 23);
+}
+// A finite value scale above all so far: the power of two above it, and the bound of ev.
+__device__ __forceinline__ void raise_top(float va, float& vtop, float& least) {
+  const int e = min(254, (int)(__float_as_uint(va) >> 23) + 1);
+  vtop = __int_as_float(e << 23);
+  least = fmaxf(kLeastRef, (float)(e - 127) - kFar);
+}
+// A row's ev for the largest product 2^d.
+__device__ __forceinline__ float row_ref(float d, float least) {
+  return fminf(fmaxf(ceilf(d), least), kMostRef);
+}
 
 // 16-key slots of a warp's ring: one being read, the others in flight.  12 KB a warp
 // at D = 128: 12 warps of an SM have 96 KB under way.  (256 single tokens x 8 heads x
@@ -473,12 +493,15 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
     // acc[i][t]: rows 8 i + 2c, 8 i + 2c + 1 of the lane's dims 2t, then of 2t + 1
     float acc[NR][D / 16][4];
     float m[NR][2], l[NR][2];  // running maxima (log2 units), sums over this lane's keys
-    float vref = 0.f;          // power of two above the value scales seen
-    float weight = 0.f;        // kWeightScale / vref
+    float d[NR][2];            // log2 of the largest p * value scale, and kSlack
+    float wt[NR][2];           // 2^7 / 2^ev
+    float vtop = 0.f, least = kLeastRef;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       m[i][0] = m[i][1] = -CUDART_INF_F;
       l[i][0] = l[i][1] = 0.f;
+      d[i][0] = d[i][1] = -CUDART_INF_F;
+      wt[i][0] = wt[i][1] = 1.f;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) acc[i][t][0] = acc[i][t][1] = acc[i][t][2] = acc[i][t][3] = 0.f;
     }
@@ -553,6 +576,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
       }
       float f[NR][2], mx[NR][2];
       bool up = false;
+      const float va = fabsf(vs), lva = log2_fast(va);
 #pragma unroll
       for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -560,19 +584,12 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
           f[i][k] = __fmul_rn(inv[i][k], ks);
           mx[i][k] = fmaxf(sc[i][k], sc[i][k + 2]);
           mx[i][k] = mx[i][k] == -CUDART_INF_F ? mx[i][k] : __fmul_rn(mx[i][k], f[i][k]);
-          up |= mx[i][k] > m[i][k] + kSlack;
+          const float x = mx[i][k] - m[i][k];  // NaN where nothing has been seen: not up
+          up |= x > kSlack || x + lva > d[i][k];
         }
-      const float va = fabsf(vs);
-      const bool vup = va > vref && va < CUDART_INF_F;
+      const bool vup = va > vtop && va < CUDART_INF_F;
       if (__any_sync(kAll, up || vup)) {
-        float beta = 1.f;
-        if (vup) {  // the next power of two, twice the largest scale at most
-          const int e = (int)(__float_as_uint(va) >> 23) + 1;
-          const float to = __int_as_float(max(kLeastRef, min(254, e)) << 23);
-          beta = __fdiv_rn(vref, to);
-          vref = to;
-          weight = __fdiv_rn(kWeightScale, vref);
-        }
+        if (vup) raise_top(va, vtop, least);
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
           float g[2];
@@ -584,9 +601,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
             x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
             const float to = fmaxf(m[i][k], x);
             const float alpha = to == m[i][k] ? 1.f : exp2_fast(m[i][k] - to);
+            if (to != m[i][k]) d[i][k] += m[i][k] - to;
+            d[i][k] = fmaxf(d[i][k], x - to + (lva + kSlack));
             m[i][k] = to;
             l[i][k] = __fmul_rn(l[i][k], alpha);
-            g[k] = __fmul_rn(alpha, beta);
+            const float w = exp2_whole(7.f - row_ref(d[i][k] - kSlack, least));
+            g[k] = __fmul_rn(alpha, __fdiv_rn(w, wt[i][k]));
+            wt[i][k] = w;
           }
 #pragma unroll
           for (int t = 0; t < D / 16; ++t)
@@ -594,7 +615,6 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
             for (int e = 0; e < 4; ++e) acc[i][t][e] = __fmul_rn(acc[i][t][e], g[e & 1]);
         }
       }
-      const float pv = __fmul_rn(weight, vs);
       uint32_t pb[NP][NR][2];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
@@ -610,7 +630,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
         l[i][1] = __fadd_rn(l[i][1], __fadd_rn(p[1], p[3]));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[e] = __fmul_rn(p[e], pv);
+          p[e] = __fmul_rn(p[e], __fmul_rn(wt[i][e & 1], vs));
           // weight 0 whatever the block's scale is
           if (hide && (hidden >> (i * 4 + e) & 1)) p[e] = 0.f;
         }
@@ -650,7 +670,6 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
     // ---- results: lane (r, c) holds dims r * D / 8 .. of rows 8 i + 2c + j
     const bool begins = u0 == 0, ends = u1 == units;
     const bool whole = begins && ends;
-    const float unit = __fmul_rn(vref, 1.f / kWeightScale);
     float* part = a.parts + ((int64_t)worker * 2 + (begins ? 1 : 0)) * R * (D + 2);
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
@@ -664,7 +683,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : 
         L += __shfl_xor_sync(kAll, L, 16);
         if (row >= n_rows) continue;
         // the mean, also of a part (sums of large values would overflow), in two steps, since
-        // unit / L can underflow; a row that saw no key has an all-zero accumulator
+        // 1 / (wt L) can underflow; a row that saw no key has an all-zero accumulator
+        const float unit = __fdiv_rn(1.f, wt[i][j]);
         const float g = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
         const int at = first_row + row, t = at / a.G;
         const int hq = h * a.G + at - t * a.G;

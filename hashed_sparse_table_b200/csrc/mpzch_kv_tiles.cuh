@@ -29,7 +29,7 @@ struct TileSmem {
   static constexpr int kV = kK + kTileStages * kOperand;
   static constexpr int kRaw = kV + kTileStages * kOperand;
   static constexpr int kSmall = kRaw + kRawSlots * kRawKeys * D;
-  static constexpr int kBytes = kSmall + 6144 + 1024;  // and up to 1 KB to align the base
+  static constexpr int kBytes = kSmall + 8192 + 1024;  // and up to 1 KB to align the base
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -310,9 +310,10 @@ struct TileSmall {
   long long sums[kTileThreads / 32];
   // [half][columns][row], read by the row's other thread; maxima are written again only
   // behind the next step's barrier, sums behind the next item's
-  float swap_max[2][2][128], swap_sum[2][2][128];
+  float2 swap_max[2][2][128];  // and the largest p * value scale over it, log2
+  float swap_sum[2][2][128];
 };
-static_assert(sizeof(TileSmall) <= 6144);
+static_assert(sizeof(TileSmall) <= 8192);
 
 __device__ __forceinline__ bool any_of_256(int id, bool x) {
   uint32_t r;
@@ -383,10 +384,10 @@ constexpr uint32_t kOffPlus2 = 0xE480E480u, kOffMinus2 = 0x64806480u;  // -1152,
 // copies and smaller code (the roles together overran the instruction cache) 513;
 // queries copied under the last step 373; two threads a row 283; item cost in the shares
 // 250; products issued from warp-uniform code 233.  Scales: the score factor holds the key scale (one for 16
-// keys); the value scale goes into the exponent, p 2^7 scale / vref =
-// 2^(s - m + log2(..)), and the row sum takes it out again once in 16 keys, so neither
-// costs work per element.  O is rescaled only when a row's maximum rises by more than
-// 2^kSlack or vref changes.
+// keys); the value scale goes into the exponent, p 2^7 scale / 2^ev =
+// 2^(s - m + log2(scale) + 7 - ev), and the row sum takes it out again once in 16 keys, so
+// neither costs work per element.  O is rescaled only when a row's maximum or its largest
+// product p * scale, which ev follows, rises by more than 2^kSlack.
 // The loader warp also walks the block's items and hands them to the others.  A wait
 // that runs out marks the launch failed and lets every role run to its end without
 // further waits, so that all named barriers are met.
@@ -577,7 +578,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       }
       float m = -CUDART_INF_F, sum = 0.f;
       bool seen = false;             // a key of this share
-      float vref = 0.f, lref = 0.f;  // power of two above the value scales, its log2
+      float d = -CUDART_INF_F, ev = 0.f;  // log2 of the largest p * value scale, reference
+      float vtop = 0.f, least = kLeastRef;
 #pragma unroll 1
       for (int j = 0; j < item.steps; ++j, ++n_k) {
         const int key = item.key0 + j * kTileKeys + part * 64;
@@ -608,7 +610,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
         };
         // ---- largest score.  The loops over 32 keys stay loops: unrolled, the block's
         // roles together overran the instruction cache.
-        float mx = -CUDART_INF_F;
+        float mx = -CUDART_INF_F, mv = -CUDART_INF_F;  // (mv: over 2^mx)
 #pragma unroll 1
         for (int cnk = 0; cnk < 2; ++cnk) {
           uint32_t y[32];
@@ -620,6 +622,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = vis >> e & 1 ? y[e] : 0xFF800000u;
           }
+          float top[2];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float f = __fmul_rn(inv, scale[cnk * 2 + g].x);
@@ -627,29 +630,31 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
             float best = max3(max3(z[0], z[1], z[2]), max3(z[3], z[4], z[5]), max3(z[6], z[7], z[8]));
             best = max3(best, max3(z[9], z[10], z[11]), max3(z[12], z[13], z[14]));
             best = fmaxf(best, z[15]);
-            if (best > -CUDART_INF_F) mx = fmaxf(mx, __fmul_rn(best, f));
+            top[g] = best > -CUDART_INF_F ? __fmul_rn(best, f) : -CUDART_INF_F;
           }
+          const float to = max3(mx, top[0], top[1]);
+          mv = max3(mv + (mx - to), top[0] - to + scale[cnk * 2].y, top[1] - to + scale[cnk * 2 + 1].y);
+          mx = to;
         }
         seen |= !hide;
-        const bool vup = va > vref;
-        if (any_of_256(1 + half, mx > m + kSlack || vup)) {
-          sm->swap_max[half][part][at_row] = mx;
+        const bool vup = va > vtop;
+        if (any_of_256(1 + half, mx > m + kSlack || mx - m + mv > d + kSlack || vup)) {
+          sm->swap_max[half][part][at_row] = make_float2(mx, mv);
           sync_256(1 + half);
-          mx = fmaxf(mx, sm->swap_max[half][part ^ 1][at_row]);
-          float beta = 1.f;
-          if (vup) {
-            const uint32_t e = (__float_as_uint(va) >> 23) + 1;
-            const float to = __uint_as_float((e > 254 ? 254 : e) << 23);
-            beta = __fdiv_rn(vref, to);
-            vref = to;
-            lref = (float)((int)(e > 254 ? 254 : e) - 127);
-          }
-          const float to = fmaxf(m, mx);
+          const float2 other = sm->swap_max[half][part ^ 1][at_row];
+          const float both = fmaxf(mx, other.x);
+          mv = fmaxf(mv + (mx - both), other.y + (other.x - both));  // (NaN: no key)
+          if (vup) raise_top(va, vtop, least);
+          const float to = fmaxf(m, both);
           const float alpha = to == m ? 1.f : exp2_fast(m - to);
+          if (to != m) d += m - to;
+          d = fmaxf(d, mv + (both - to));
+          const float ev0 = ev;
+          ev = row_ref(d, least);
           m = to;
           sum = __fmul_rn(sum, alpha);
           if (j > 0) {
-            const float g = __fmul_rn(alpha, beta);
+            const float g = __fmul_rn(alpha, exp2_whole(fminf(fmaxf(ev0 - ev, -126.f), 127.f)));
 #pragma unroll 1
             for (int d = 0; d < D / 2; d += 32) {
               uint32_t x[32];
@@ -677,8 +682,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
           for (int g = 0; g < 2; ++g) {
             const float2 sc = scale[cnk * 2 + g];
             f[g] = __fmul_rn(inv, sc.x);
-            // log2 of 2^7 scale / vref; far below, the weights vanish in fp16 anyway
-            const float x = __fadd_rn(__fsub_rn(sc.y, lref), 7.f);
+            // log2 of 2^7 scale / 2^ev; far below, the weights vanish in fp16 anyway
+            const float x = __fadd_rn(__fsub_rn(sc.y, ev), 7.f);
             lp[g] = x < -60.f ? -60.f : x;
           }
           tmem_loaded(y);
@@ -746,7 +751,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv_tiles(AttendArgs a) {
       __syncwarp();
       tc_fence_after();
       const int hq = item.h * a.G + (real ? row - t * a.G : 0);
-      const float unit = __fmul_rn(vref, 1.f / kWeightScale);
+      const float unit = exp2_whole(ev - 7.f);
       // the mean, also of a part, in two steps, since unit / sum can underflow
       const float g = __fdiv_rn(1.f, sum);
       const int prow = half * 128 + at_row;

@@ -350,8 +350,9 @@ MPZCH_API int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, i
  * Arithmetic: scores, maxima, sums and accumulators in fp32.  Products take 16-bit
  * operands: the codes exactly; F16 and BF16 queries exactly (below 2^113 in size, past
  * which a row may give NaN), F32 ones in two parts, 22 bits, after a power-of-two scaling
- * of the row; softmax weights rounded to fp16 (F32 and F16: in two parts), where weights
- * below 2^-21 of the largest lose bits and those below 2^-32 vanish.
+ * of the row; softmax weights times their block's value scale rounded to fp16 (F32 and F16:
+ * in two parts), where products below 2^-21 of the row's largest lose bits and those below
+ * 2^-32 of it vanish (as do those below 2^-132 of the largest scale met, or below 2^-151).
  * Scales may be zero or negative.  A query row with a NaN or an infinity that sees a key
  * gives NaN; a scale that is NaN gives NaN to the rows that see a key of its block, an
  * infinite one what infinite scores or values leave; other rows do not notice.  Results

@@ -1,5 +1,6 @@
 """History cache on the GPU at the ends of its number ranges: value scales near the smallest and
-the largest numbers of binary32, and held codes under negative scales."""
+the largest numbers of binary32, held codes under negative scales, and weights that lie in blocks
+far smaller than their neighbours."""
 import numpy as np
 import pytest
 import torch
@@ -98,3 +99,88 @@ def test_attend_largest_values(kv, kind, rows, length):
     assert np.abs(want).max() > 2.0**126
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= bound(want, s, length, 64, kind)).all()
+
+
+# ------------------------------------------------------------------ attention: uneven scales
+def products(c, scale, causal=False):
+    """The largest of (softmax weight times value scale) over the keys of each row and head, times
+    the sum of |code| over the keys: what bounds the bits that weights lose below fp16's normal
+    numbers when their reference is the row's own largest product."""
+    q = c["q"].double().numpy()
+    n, Hq, D = q.shape
+    H, bs = c["kc"].shape[1:3]
+    low = np.zeros(q.shape)
+    for b, L in enumerate(c["seq"]):
+        s, e = int(c["cu"][b]), int(c["cu"][b + 1])
+        ids = c["table"][b, :-(-int(L) // bs)]
+        pos = int(L) - (e - s) + np.arange(e - s)[:, None]
+        for hq in range(Hq):
+            h = hq // (Hq // H)
+            k = (c["kc"][ids, h].astype(float) * c["ks"][ids, h].astype(float)[:, None, None])
+            z = scale * q[s:e, hq] @ k.reshape(-1, D)[:L].T
+            if causal:
+                z = np.where(np.arange(L)[None] <= pos, z, -np.inf)
+            p = np.exp(z - z.max(1, keepdims=True))
+            sees = np.isfinite(z)
+            p /= p.sum(1, keepdims=True)
+            each = np.repeat(np.abs(c["vs"][ids, h].astype(float)), bs)[:L]
+            codes = np.abs(c["vc"][ids, h].astype(float)).reshape(-1, D)[:L]
+            low[s:e, hq] = (p * each).max(1)[:, None] * (sees @ codes)
+    return low
+
+
+def leaning(seed, lens, rows, kind, gap, Hq=2, H=2, order=1):
+    """A history in which the first or the second half of a request's blocks holds the keys that a
+    row attends to: even rows look at small blocks, odd ones at large ones, whose value scales are
+    2^gap apart, and a score of about 40 (in log2 units) lies between the two kinds of keys."""
+    c = history(seed, lens, [rows] * len(lens), Hq, H, 64, 16, kind)
+    sign = 1 - 2 * (np.arange(len(c["q"])) % 2)
+    q = c["q"].float() * 0.1
+    q[:, :, 0] = torch.from_numpy(4.0 * sign).float()[:, None]
+    c["q"] = q.to(c["q"].dtype)
+    for b, L in enumerate(lens):
+        n = -(-L // 16)
+        ids = c["table"][b, :n]
+        small = np.arange(n) % 2 == 0 if order == 0 else (np.arange(n) < n // 2) == (order > 0)
+        c["kc"][ids[small], :, :, 0] = 127
+        c["kc"][ids[~small], :, :, 0] = -127
+        c["ks"][ids] = 0.2
+        c["vs"][ids] = (np.where(small, 2.0**-gap, 1.0)[:, None]
+                        * (1 + 0.3 * np.arange(n) / n)[:, None]).astype(np.float32)
+    return c
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 2, 40, 150])
+@pytest.mark.parametrize("gap", [13, 24, 36])
+@pytest.mark.parametrize("order", [1, -1, 0])
+def test_attend_weights_in_blocks_of_small_scale(kv, kind, rows, gap, order):
+    """Nearly all weight lies on keys whose values are 2^gap below those of their neighbours, in
+    front of them, behind them and in turn: the output keeps the small values' bits, and rows of
+    the same tile that look at the large ones keep theirs."""
+    c = leaning(53, [300, 2000, 33], rows, kind, gap, order=order)
+    got, want, s = attend(kv, c, scale=0.15)
+    low = products(c, 0.15)
+    # weights in fp16 parts end at 2^-32 of the row's largest product
+    off = bound(want, s, 2000, 64, kind, low)
+    assert (np.abs(got - want) <= off).all(), np.max(np.abs(got - want) / off)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_attend_large_values_that_later_scores_outweigh(kv, kind, rows):
+    """Scores that rise from block to block by hundreds while the value scales fall: what came
+    first is large but has no weight in the end."""
+    for scale in (0.05, 1.0, 20.0):
+        c = history(54, [900, 60], [rows] * 2, 2, 2, 64, 16, kind)
+        c["q"] = (torch.ones_like(c["q"]) + 0.01 * c["q"].float()).to(c["q"].dtype)
+        for b, n in enumerate((57, 4)):
+            ids = c["table"][b, :n]
+            c["kc"][ids] = (np.linspace(-100, 100, n)[:, None, None, None]
+                            + np.random.default_rng(55).integers(-20, 20, c["kc"][ids].shape)).astype(np.int8)
+            c["ks"][ids] = 0.02
+            c["vs"][ids] = np.float32(2.0) ** np.linspace(20, -20, n)[:, None]
+        got, want, s = attend(kv, c, scale=scale)
+        low = products(c, scale)
+        off = bound(want, s, 900, 64, kind, low)
+        assert (np.abs(got - want) <= off).all(), (scale, np.max(np.abs(got - want) / off))
