@@ -648,7 +648,8 @@ def mpzch_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, 
 class MpzchHistory:
     """An int8 history cache (codes and scales as torch tensors) with its list of free blocks and
     the requests' block tables; methods forward to the entry points above, on the current
-    stream (their results come from torch's allocator for it)."""
+    stream (their results come from torch's allocator for it).  What it keeps is updated in
+    place, so a captured step goes on, at every replay, from what the last step left."""
 
     def __init__(self, num_blocks: int, block_size: int, kv_heads: int, dim: int,
                  max_requests: int, max_blocks: int):
@@ -676,7 +677,8 @@ class MpzchHistory:
         seq, left = torch.empty_like(self.seq_len), torch.empty_like(self.free_count)
         mpzch_kv_tables(self.seq_len, new_len, self.block_size, self.free_blocks, self.free_count,
                         self.block_table, cu, seq, slots, left, self.status)
-        self.seq_len, self.free_count = seq, left
+        self.seq_len.copy_(seq)
+        self.free_count.copy_(left)
         return cu, slots
 
     def append(self, k, v, slots):
