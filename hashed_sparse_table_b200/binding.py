@@ -685,6 +685,8 @@ class MpzchHistory:
         mpzch_kv_append(k, v, slots, *self.cache(), self.status)
 
     def attend(self, q, cu_new, max_new: int, out=None, **options):
+        if out is None and options.get("stream") is not None:
+            raise ValueError("a call with a stream of its own needs an output too")
         out = torch.empty_like(q) if out is None else out
         mpzch_kv_attend(q, *self.cache(), self.block_table, cu_new, self.seq_len, max_new, out,
                         status=self.status, **options)

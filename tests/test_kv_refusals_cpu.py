@@ -25,3 +25,13 @@ def test_outputs_whose_heads_overlap_are_refused(lib, n, H):
         assert attend(lib, n=n, Hq=H, H=1, D=32, osn=sn, osh=sh) == EINVAL, (sn, sh)
     # not a matter of each stride alone
     assert (32, 32) in pairs and (40, 40) in pairs
+
+
+def test_history_attend_on_a_stream_of_its_own_needs_an_output():
+    """An output from torch's allocator belongs to the current stream."""
+    import torch
+    from hashed_sparse_table_b200 import binding
+    h = object.__new__(binding.MpzchHistory)
+    q = torch.zeros((1, 2, 64))
+    with pytest.raises(ValueError, match="output"):
+        h.attend(q, None, 1, stream=object(), workspace=q)
