@@ -500,6 +500,13 @@ def _kv_opt(t, dtype, device: int) -> bool:
     return t is None or _kv_ok(t, dtype, device)
 
 
+def _kv_int(name: str, x: int) -> int:
+    """x, which ctypes would cut to 32 bits."""
+    if not -2**31 <= x < 2**31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 def _kv_stream(stream, device: int):
     """The raw stream of a history call; torch's Stream object is not built for the current one."""
     if stream is None:
@@ -564,7 +571,8 @@ def mpzch_kv_tables(cached_len, new_len, block_size: int, free_blocks, free_coun
         raise ValueError(f"{n} requests need new_len [{n}], block_table [{n}, blocks], cu_new "
                          f"[{n + 1}], seq_len [{n}] and counts of one value")
     rc = _lib.mpzch_kv_tables(
-        cached_len.data_ptr(), new_len.data_ptr(), n, block_size, free_blocks.data_ptr(),
+        cached_len.data_ptr(), new_len.data_ptr(), n, _kv_int("block_size", block_size),
+        free_blocks.data_ptr(),
         free_blocks.numel(), free_count.data_ptr(), block_table.data_ptr(), table[1],
         cu_new.data_ptr(), seq_len.data_ptr(), slots.data_ptr(), slots.numel(),
         free_count_out.data_ptr(), None if status is None else status.data_ptr(),
@@ -637,8 +645,9 @@ def mpzch_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, 
     rc = _lib.mpzch_kv_attend(
         q.data_ptr(), q_n, q_h, n, code, k_cache.data_ptr(), v_cache.data_ptr(),
         k_scale.data_ptr(), v_scale.data_ptr(), blocks, block_size, q_heads, heads, dim,
-        block_table.data_ptr(), table[1], cu_new.data_ptr(), seq_len.data_ptr(), b, max_new,
-        dim ** -0.5 if softmax_scale is None else softmax_scale, 1 if causal else 0, window,
+        block_table.data_ptr(), table[1], cu_new.data_ptr(), seq_len.data_ptr(), b,
+        _kv_int("max_new", max_new), dim ** -0.5 if softmax_scale is None else softmax_scale,
+        1 if causal else 0, _kv_int("window", window),
         out.data_ptr(), o_n, o_h, None if lse is None else lse.data_ptr(), workspace.data_ptr(),
         workspace.numel(), None if status is None else status.data_ptr(),
         _kv_stream(stream, device))

@@ -35,3 +35,37 @@ def test_history_attend_on_a_stream_of_its_own_needs_an_output():
     q = torch.zeros((1, 2, 64))
     with pytest.raises(ValueError, match="output"):
         h.attend(q, None, 1, stream=object(), workspace=q)
+
+
+def test_whole_numbers_past_32_bits_are_refused(monkeypatch):
+    """ctypes drops the upper bits, so a window of 2^32 + 5 was one of 5.  (CPU tensors on a
+    current device of -1; what is refused never reaches the library.)"""
+    import torch
+    from hashed_sparse_table_b200 import binding
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(args) or 0
+    monkeypatch.setattr(binding, "_lib", Lib())
+    i32, i64 = torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
+    cu, table = torch.zeros(3, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int32)
+    cache, scale = torch.zeros((3, 2, 16, 64), dtype=torch.int8), torch.zeros((3, 2))
+    q, ws = torch.zeros((2, 2, 64)), torch.zeros(256, dtype=torch.uint8)
+
+    def attend(max_new=1, window=0):
+        binding.mpzch_kv_attend(q, cache, cache, scale, scale, table, cu, i32, max_new, q.clone(),
+                                window=window, workspace=ws, stream=0)
+
+    def tables(block_size):
+        binding.mpzch_kv_tables(i32, i32, block_size, i32, i64, table, cu, i32, i64, i64, stream=0)
+
+    attend(window=2**31 - 1)
+    tables(16)
+    assert len(calls) == 2
+    for call in (lambda x: attend(window=x), lambda x: attend(max_new=x), tables):
+        for x in (2**31, 2**32 + 16, -2**32 + 16, 2**70):
+            with pytest.raises(ValueError, match="32 bits"):
+                call(x)
+    assert len(calls) == 2
