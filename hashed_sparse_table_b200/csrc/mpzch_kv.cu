@@ -168,8 +168,8 @@ int mpzch_kv_tables(const int32_t* cached_len, const int32_t* new_len, int32_t n
                     int32_t* cu_new, int32_t* seq_len, int64_t* slots, int64_t n_slots,
                     int64_t* free_count_out, int32_t* dev_status, void* stream) {
   if (n_requests < 0 || n_requests > MPZCH_KV_MAX_REQUESTS || !block_size_ok(block_size) ||
-      n_free_blocks < 0 || n_free_blocks >= kMaxInt || max_blocks < 0 || n_slots < 0 ||
-      n_slots >= kMaxInt)
+      n_free_blocks < 0 || n_free_blocks >= kMaxInt || max_blocks < 0 ||
+      (int64_t)max_blocks * block_size > kMaxInt - 1024 || n_slots < 0 || n_slots >= kMaxInt)
     return MPZCH_EINVAL;
   if (!free_count || !free_count_out || free_count == free_count_out || !cu_new ||
       (n_free_blocks > 0 && !free_blocks) || (n_slots > 0 && !slots))

@@ -299,7 +299,8 @@ MPZCH_API int mpzch_serve_gather(const int64_t* snap_keys, int64_t capacity, int
  *                  the list; given-back blocks are appended there).
  * cached_len, new_len: device int32[B], B = n_requests <= MPZCH_KV_MAX_REQUESTS;
  * free_blocks: device int32[n_free_blocks]; free_count: device int64, taken as
- * at most n_free_blocks.  The outputs must not alias the inputs. */
+ * at most n_free_blocks.  max_blocks * block_size stays below 2^31 - 1024.  The outputs
+ * must not alias the inputs. */
 MPZCH_API int mpzch_kv_tables(const int32_t* cached_len, const int32_t* new_len, int32_t n_requests,
                               int32_t block_size, const int32_t* free_blocks, int64_t n_free_blocks,
                               const int64_t* free_count, int32_t* block_table, int32_t max_blocks,

@@ -5,7 +5,7 @@ import itertools
 import numpy as np
 import pytest
 
-from test_kv_cpu import EINVAL, attend, lib  # noqa: F401 (lib: fixture)
+from test_kv_cpu import EINVAL, attend, lib, tables  # noqa: F401 (lib: fixture)
 
 
 def overlapping(n, sn, h, sh, dim):
@@ -69,3 +69,13 @@ def test_whole_numbers_past_32_bits_are_refused(monkeypatch):
             with pytest.raises(ValueError, match="32 bits"):
                 call(x)
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("bs,most", [(16, 2**27 - 64), (32, 2**26 - 32), (128, 2**24 - 8)])
+def test_tables_whose_lengths_would_pass_31_bits_are_refused(lib, bs, most):
+    """The same limit as attention's: max_blocks * block_size below 2^31 - 1024 (lengths are
+    int32: with more blocks c + w could come back negative)."""
+    assert most * bs == 2**31 - 1024
+    for blocks in (most, most + 1, 2**27, 2**31 - 1):
+        assert tables(lib, bs=bs, max_blocks=blocks) == EINVAL, blocks
+        assert attend(lib, bs=bs, max_blocks=blocks) == EINVAL, blocks
