@@ -611,7 +611,7 @@ def mpzch_kv_attend(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_new, 
                     window: int = 0, lse=None, workspace=None, status=None, stream=None) -> None:
     """Attention of q [n, q_heads, dim] over the cached histories into out (same shape and type;
     include/mpzch.h).  softmax_scale: dim ** -0.5 unless given.  max_new: a bound on the rows of
-    one request.  workspace: uint8, mpzch_kv_attend_workspace bytes; taken from torch's allocator
+    one request, which chooses the kernel for all of them.  workspace: uint8, mpzch_kv_attend_workspace bytes; taken from torch's allocator
     for the current stream unless given."""
     device = torch.cuda.current_device()
     blocks, heads, block_size, dim = _kv_cache(device, k_cache, v_cache, k_scale, v_scale)
@@ -658,7 +658,11 @@ class MpzchHistory:
     """An int8 history cache (codes and scales as torch tensors) with its list of free blocks and
     the requests' block tables; methods forward to the entry points above, on the current
     stream (their results come from torch's allocator for it).  What it keeps is updated in
-    place, so a captured step goes on, at every replay, from what the last step left."""
+    place, so a captured step goes on, at every replay, from what the last step left.
+
+    There is no call that ends a request.  Its blocks are given back by writing their ids behind
+    the first free_count entries of free_blocks, adding their number to free_count and setting the
+    request's seq_len to 0, all in place."""
 
     def __init__(self, num_blocks: int, block_size: int, kv_heads: int, dim: int,
                  max_requests: int, max_blocks: int):

@@ -38,14 +38,6 @@ __device__ __forceinline__ void pdl_trigger() {
 
 __device__ __forceinline__ void pdl_enter() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// int8 export rule.
-// q = rne(fl(x / s)), clamped to +-127.  Fast path: p = fl(x * fl(1/s)) differs
-// from the exact quotient t = x/s by at most |t| 2^-23 + |t| 2^-24, and fl(t)
-// from t by at most |t| 2^-24, so |p - fl(x/s)| < |t| 2^-22 <= 127.00001 * 2^-22
-// < 3.1e-5.  When p is more than 1e-4 away from every half-integer, fl(x/s)
-// rounds to the same integer as p; otherwise the IEEE division is taken.  (A
-// reciprocal that is not finite, for a subnormal s, sends every element to
-// the division.)
 // Round-half-to-even of |v| < 2^22 without a conversion instruction: adding
 // 1.5 * 2^23 leaves v's nearest integer (ties to even, IEEE rounding of the
 // add) in the low mantissa bits, and subtracting it again gives that integer as
@@ -57,10 +49,13 @@ __device__ __forceinline__ int rne_small(float v) {
   return __float_as_int(__fadd_rn(v, kRoundMagic)) - kRoundMagicBits;
 }
 
-// int8 code of x / s for the values of one lane.  The product p = x * fl(1/s)
-// is within 3.1e-5 of x / s, so rne(p) = rne(x / s) whenever p lies at least
-// 1e-4 from a half-integer; a lane with any value closer than that (or with no
-// usable reciprocal) recomputes all of its values from the IEEE quotient.
+// int8 export rule, q = rne(fl(x / s)) clamped to +-127, for the values of one
+// lane.  p = fl(x * fl(1/s)) differs from the exact quotient t = x/s by at most
+// |t| 2^-23 + |t| 2^-24, and fl(t) from t by at most |t| 2^-24, so
+// |p - fl(x/s)| < |t| 2^-22 <= 127.00001 * 2^-22 < 3.1e-5.  When p is more than
+// 1e-4 away from every half-integer, fl(x/s) rounds to the same integer as p; a
+// lane with any value closer than that (or with no usable reciprocal, for a
+// subnormal s) recomputes all of its values from the IEEE quotient.
 // |x| <= a = 127 s, so every code lies in [-127, 127] (clamped all the same).
 template <int kN>
 __device__ __forceinline__ void quant_lane(const float (&x)[kN], float s, float rcp, bool fast,

@@ -102,7 +102,8 @@ int launch_tiles(const AttendArgs& a, cudaStream_t st) {
   return rc;
 }
 
-// Histories up to kWholeKeys of few items (request, kv head) go whole to a warp each: its
+// What the table has room for decides, since the host knows no length: where that is
+// kWholeKeys at most and the items (request, kv head) are few, each goes whole to a warp: its
 // 32 steps take about as long as the launch that would join the parts of cut ones (4
 // requests x 8 heads of up to 300 keys, dim 64, on the device: one launch 11.5 us, cut and
 // joined 8.5 + 5.1 us; and a caller issues one launch fewer, 16.6 against 18.5 us a call).
@@ -152,6 +153,11 @@ int launch_rows(const AttendArgs& a, cudaStream_t st) {
   return rows <= 8 ? launch_rows<D, T, 8, NQ, NP>(a, st) : launch_rows<D, T, 16, NQ, NP>(a, st);
 }
 
+// NQ, NP: fp16 parts of the queries and of the weights.  16-bit queries fit one part (rows
+// are scaled by a power of two).  Weights in one part, 11 bits, are what bf16 results get:
+// single tokens of 256 requests are then 1.670e-3 from 64 bits (relative, over all
+// outputs) where weights in 32 bits give 1.656e-3, nearly all of both the rounding of the
+// result; fp16 results would be 1.4 times as far as that rounding, so they take two.
 template <typename T, int NQ, int NP>
 int launch_rows_dim(const AttendArgs& a, int dim, cudaStream_t st) {
   return dim == 32 ? launch_rows<32, T, NQ, NP>(a, st)

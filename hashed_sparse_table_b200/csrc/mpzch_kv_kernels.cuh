@@ -348,10 +348,11 @@ __device__ __forceinline__ uint4 codes16(const uint64_t (&x)[8], float s, float 
 // works through the runs that begin there.  A lane handles 16 values of a token, a warp
 // 4 x 32 * 16 / D tokens, all of its loads in flight together; W is what a whole block
 // of tokens needs, so every value is read once and waits in registers for the maximum.
-// Bound by HBM once a batch is long: 104 thousand bf16 tokens x 8 heads x 128 in 32-token
-// blocks (849 MB) 170 us, 5.0 TB/s, 0.76 of the measured copy rate; 31 thousand fp32
-// tokens x 4 heads x 128 in 64-token blocks (176 MB) 48 us, 3.7 TB/s, where the few runs a
-// group has leave the latency of slots, values and barrier open.  256 single tokens of 8
+// A long batch is near HBM and near its issue slots: 104 thousand bf16 tokens x 8 heads x
+// 128 in 32-token blocks (849 MB) 177 us a call, 4.8 TB/s, 0.73 of the measured copy rate,
+// instructions issued in 0.55 of the cycles; a warp's runs follow one another, so each
+// one's loads wait in the open.  31 thousand fp32 tokens x 4 heads x 128 in 64-token blocks
+// (176 MB) 44 us, 4.0 TB/s, where a group has few runs.  256 single tokens of 8
 // heads x 64 take 3.9 us in a graph.  Measured and dropped: half the passes kept and
 // twice the warps (the per-run work doubled: 217 -> 247 us), and the export's test for
 // nearly half-way products, which 16-bit values fail in nearly every warp (260 us).

@@ -264,10 +264,10 @@ __device__ __forceinline__ void store_row(T* p, const float (&x)[N]) {
 // keys 2c, 2c+1, 2c+8, 2c+9 and D / 8 neighbouring dims, two to each 16-dim tile.
 // Bound by HBM and, close behind, by issuing about 450 instructions for 4 KB of codes
 // (turning a byte into fp16 is one byte permutation and one subtraction for two): 256
-// tokens, 32 query and 8 kv heads x 128, 515 MB of cache, 108 us with the join, 4.8 TB/s,
-// 0.73 of the measured copy rate; two histories of 78 and 110 thousand keys, 4 kv heads x
-// 128, fp16, 193 MB, 48 us; 4,096 fp32 histories of up to 1,000 keys, 4 heads x 128, 625 MB,
-// 201 us (two products for each, and half of the time in beginning and ending items).
+// tokens, 32 query and 8 kv heads x 128, 515 MB of cache, 110 us with the join, 4.7 TB/s,
+// 0.72 of the measured copy rate; two histories of 78 and 110 thousand keys, 4 kv heads x
+// 128, fp16, 193 MB, 49 us; 4,096 fp32 histories of up to 1,000 keys, 4 heads x 128, 625 MB,
+// 204 us (two products for each, and half of the time in beginning and ending items).
 template <int D, typename T, int R, int NQ, int NP>
 __global__ void __launch_bounds__(32 * kRowWarps, R == 8 ? (D == 128 ? 3 : 4) : NQ == 1 ? 3 : 2)
     k_kv_rows(AttendArgs a) {

@@ -199,7 +199,7 @@ __device__ __forceinline__ TileRange tile_range(const AttendArgs& a, const Reque
 
 // Beginning and ending an item (queries, result) costs a block about as much as this
 // many steps; shares count an item as kItemCost + steps.  (The chunks and the candidates
-// named below: 1 gives 249 and 244 us, 2 226 and 222, 3 225 and 235, 4 229 and 246.)
+// named below: 1 gives 247 and 258 us, 2 226 and 255, 3 228 and 270, 4 232 and 281.)
 constexpr int kItemCost = 2;
 
 // Walks the items (request, kv head, row tile) of a block's share of the work, the
@@ -378,9 +378,9 @@ constexpr uint32_t kOffPlus2 = 0xE480E480u, kOffMinus2 = 0x64806480u;  // -1152,
 // 3,600 cycles of softmax (of which the exponentials, 4 lanes a cycle and scheduler
 // shared by four warps, take 1,550), then 1,300 of its two products and 600 of signals,
 // of 6,000 in all; the tensor pipe is busy 0.30 of the time.  Six chunks of 500 to 4,096
-// rows behind up to 8,000 keys, 16 query and 4 kv heads x 128, bf16 (133 GFLOP): 227 us,
-// 585 TFLOP/s, 0.36 of the measured matrix rate; 32 x 1,024 candidates, 8 heads x 64, fp16
-// (72 GFLOP): 253 us (222 before the weights' second part).  What it went through: one thread a row with 128 keys 660 us; bulk
+// rows behind up to 8,000 keys, 16 query and 4 kv heads x 128, bf16 (133 GFLOP): 226 us,
+// 590 TFLOP/s, 0.36 of the measured matrix rate; 32 x 1,024 candidates, 8 heads x 64, fp16
+// (72 GFLOP): 255 us (222 before the weights' second part).  What it went through: one thread a row with 128 keys 660 us; bulk
 // copies and smaller code (the roles together overran the instruction cache) 513;
 // queries copied under the last step 373; two threads a row 283; item cost in the shares
 // 250; products issued from warp-uniform code 233.  Scales: the score factor holds the key scale (one for 16

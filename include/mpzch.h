@@ -344,20 +344,24 @@ MPZCH_API int64_t mpzch_kv_attend_workspace(int32_t q_heads, int32_t kv_heads, i
  * that lay one head of out on another are refused (MPZCH_EINVAL).
  * Rows from cu_new[B] on are neither read nor written.  max_new: the caller's
  * bound on a request's rows; it chooses kernels and changes no result beyond
- * rounding.  n * q_heads and max_blocks * block_size stay below 2^31 - 1024.
+ * rounding.  The choice is one for the whole call: a loose bound, or one long request
+ * among single tokens, sends all of them to the kernel for many rows, where a single
+ * token costs as much as 128 rows.  n * q_heads and max_blocks * block_size stay below 2^31 - 1024.
  * Key positions come through block_table (int32[B][max_blocks]); a block id
  * outside the cache hides its keys (MPZCH_STATUS_BADBLOCK), a length past
  * max_blocks * block_size or a cu_new outside 0..n is cut (MPZCH_STATUS_BADLEN).
  * Arithmetic: scores, maxima, sums and accumulators in fp32.  Products take 16-bit
- * operands: the codes exactly; F16 and BF16 queries exactly (below 2^113 in size, past
- * which a row may give NaN), F32 ones in two parts, 22 bits, after a power-of-two scaling
- * of the row; softmax weights times their block's value scale rounded to fp16 (F32 and F16:
+ * operands: the codes exactly; F16 and BF16 queries exactly but for what lies below 2^-38
+ * of the row's largest (BF16 below 2^113 in size, past which a row may give NaN), F32 ones
+ * in two parts, 22 bits, after a power-of-two scaling of the row; softmax weights times their block's value scale rounded to fp16 (F32 and F16:
  * in two parts), where products below 2^-21 of the row's largest lose bits and those below
  * 2^-32 of it vanish (as do those below 2^-132 of the largest scale met, or below 2^-151).
  * Scales may be zero or negative.  A query row with a NaN or an infinity that sees a key
  * gives NaN; a scale that is NaN gives NaN to the rows that see a key of its block, an
  * infinite one what infinite scores or values leave; other rows do not notice.  Results
- * do not depend on timing (no float atomics).
+ * do not depend on timing (no float atomics).  A wait inside the kernels that runs out
+ * (never expected) leaves wrong rows and says so in dev_status alone
+ * (MPZCH_STATUS_TIMEOUT).
  * workspace: device, 256-byte aligned, mpzch_kv_attend_workspace bytes; calls
  * that may overlap on the device need one each. */
 MPZCH_API int mpzch_kv_attend(const void* q, int64_t q_stride_n, int64_t q_stride_h, int64_t n,
