@@ -40,7 +40,8 @@ bool rows_ok(const void* p, int64_t sn, int64_t sh, int bytes) {
 // else, for each distance in heads, the two nearest distances in rows are looked at.
 bool heads_overlap(int64_t n, int64_t sn, int64_t h, int64_t sh, int64_t dim) {
   if ((n > 1 && sn < dim) || (h > 1 && sh < dim)) return true;
-  if (n <= 1 || h <= 1 || sn >= (h - 1) * sh + dim || sh >= (n - 1) * sn + dim) return false;
+  if (n <= 1 || h <= 1 || sn >= (h - 1) * sh + dim || sh >= (__int128)(n - 1) * sn + dim)
+    return false;
   for (int64_t j = 1; j < h; ++j) {
     const int64_t i = j * sh / sn, off = j * sh - i * sn;  // 0 <= off < sn
     if ((i < n && off < dim) || (i + 1 < n && sn - off < dim)) return true;

@@ -79,3 +79,10 @@ def test_tables_whose_lengths_would_pass_31_bits_are_refused(lib, bs, most):
     for blocks in (most, most + 1, 2**27, 2**31 - 1):
         assert tables(lib, bs=bs, max_blocks=blocks) == EINVAL, blocks
         assert attend(lib, bs=bs, max_blocks=blocks) == EINVAL, blocks
+
+
+def test_overlap_of_outputs_with_huge_strides_is_seen(lib):
+    """Rows times stride pass 63 bits."""
+    far = 2**39
+    for n in (2, 2**25, 2**29):
+        assert attend(lib, n=n, Hq=2, H=1, osn=far, osh=far) == EINVAL
